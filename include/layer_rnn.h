@@ -396,6 +396,86 @@ rnn_status_t rnn_debug_wf_pack(rnn_t h, void* stream, int64_t N, int layer, cons
 rnn_status_t rnn_debug_gemm_shape(int64_t M, int64_t N, int64_t K_total, int split16, int num_sms,
                                   int allow_split, int* bn, int* ksplit);
 
+/* ============================================================================
+ * Sequence-block operators: what a recurrent language model needs beside its
+ * recurrent layers.  A gated linear recurrence (parallel over time), a gated
+ * feed-forward, and a matrix-vector product with 4-bit weights for serving.
+ * The pages have no counterpart.
+ *
+ * They share one small handle (element type, flags, device status word).  The
+ * conventions above hold: caller-owned dense row-major device memory, 16-byte
+ * aligned, no overlap between arguments, asynchronous on `stream`, argument
+ * errors before anything is enqueued, no allocation but the handle's 256-byte
+ * status word at its first compute call.  RNN_F32: every tensor float32;
+ * RNN_BF16: bfloat16; recurrent states (h0, hy, dhy, dh0) are float32 in
+ * both.  Sums, states and gate arithmetic are float32 or more.
+ * ========================================================================== */
+typedef struct rnn_ops* rnn_ops_t;
+
+/* dtype: rnn_dtype_t; flags: RNN_FLAG_SYNC_CHECK or 0.  Host only. */
+rnn_status_t rnn_ops_create(rnn_ops_t* out, int dtype, uint32_t flags);
+rnn_status_t rnn_ops_destroy(rnn_ops_t h);
+/* Synchronise `stream`, then return and clear the handle's status word. */
+rnn_status_t rnn_ops_check_status(rnn_ops_t h, void* stream);
+
+/* ---- gated linear recurrence ----
+ * gx [T, N, ldg]: for each direction d the blocks p, z (and q with out_gate)
+ * of H values, direction after direction: one projection's output.
+ *   f = sigmoid(p);  h_t = f h_{t-1} + (1 - f) z;  y = h, or sigmoid(q) h
+ * Direction 1 walks t = T-1 .. 0.  num_dirs 1 or 2; y [T, N, ldy] holds
+ * [fwd || bwd]; h0, hy, dhy, dh0 [num_dirs, N, H] float32.  ldg >= D*G*H and
+ * ldy >= D*H are the row pitches in elements (0: dense), G = 2 + out_gate;
+ * elements between a row's width and its pitch are neither read nor written.
+ * lengths (device, N int32, NULL: all T): steps t >= lengths[n] leave the
+ * state unchanged and write y = 0 (dgx = 0); gx and dy are not read there.
+ * Values outside 0..T act as 0 or T.
+ * Training: pass a workspace of rnn_scan_workspace_size bytes to the forward
+ * (it keeps the state every 64 steps) and the same one, with the same gx and
+ * lengths, to the backward.  NULL workspace: inference.
+ * h0, dhy NULL = zeros; hy, dh0 NULL = not written.
+ * Any H, pitch and 16-byte aligned base; rows that start on a boundary of four
+ * elements are loaded four at a time, others one at a time.
+ * Errors: RNN_ERR_INVALID_ARG, RNN_ERR_MISALIGNED, RNN_ERR_WORKSPACE_TOO_SMALL;
+ * RNN_ERR_UNSUPPORTED for T or N * num_dirs * H of 2^31 and more. */
+rnn_status_t rnn_scan_workspace_size(rnn_ops_t h, int64_t T, int64_t N, int64_t H, int num_dirs,
+                                     int64_t* bytes);
+rnn_status_t rnn_scan_forward(rnn_ops_t h, void* stream, int64_t T, int64_t N, int64_t H,
+                              int num_dirs, int out_gate, const int32_t* lengths, const void* gx,
+                              int64_t ldg, const float* h0, void* y, int64_t ldy, float* hy,
+                              void* workspace, int64_t ws_bytes);
+/* Gradients of sum(y*dy) + sum(hy*dhy): dgx (pitch ldg), dh0.  dy has pitch
+ * ldy. */
+rnn_status_t rnn_scan_backward(rnn_ops_t h, void* stream, int64_t T, int64_t N, int64_t H,
+                               int num_dirs, int out_gate, const int32_t* lengths, const void* gx,
+                               int64_t ldg, const void* dy, int64_t ldy, const float* dhy,
+                               void* dgx, float* dh0, const void* workspace, int64_t ws_bytes);
+/* One step of direction 0 for generation: gx [N, ldg], y [N, ldy]; `state` in,
+ * `state_out` out, [N, H] float32 (the same buffer is allowed). */
+rnn_status_t rnn_scan_step(rnn_ops_t h, void* stream, int64_t N, int64_t H, int out_gate,
+                           const void* gx, int64_t ldg, const float* state, float* state_out,
+                           void* y, int64_t ldy);
+
+/* ---- matrix-vector products with 4-bit weights ----
+ * y[m][r] = sum_k x[m][k] (q[r][k] - zero[r][k / group]) scale[r][k / group]
+ * x [M, K], y [M, R]; q: R rows of ldq bytes, weight k in the low (even k) or
+ * high (odd k) half of byte k / 2, 0..15 (what lies past K in a row is
+ * ignored); scales [R, ceil(K / group)] of the handle's type; zeros the same
+ * shape, bytes 0..15, or NULL = 8 everywhere.  group: 32, 64 or 128; any K up
+ * to 65536 (the last group may be short); ldq (0: ceil(K / 2) rounded up to 16)
+ * at least ceil(K / 2) and a multiple of 16.  Meant for few tokens (M up to 16
+ * or so a pass over the weights; more run in passes of 16 at most).
+ * Every group is summed in float32 before its scale.
+ * Errors: RNN_ERR_INVALID_ARG, RNN_ERR_MISALIGNED (bases; scales need 4 or 2
+ * bytes, zeros 1), RNN_ERR_UNSUPPORTED (K > 65536, M, R of 2^31 and more). */
+rnn_status_t rnn_w4_matvec(rnn_ops_t h, void* stream, int64_t M, int64_t R, int64_t K, int group,
+                           const void* x, const uint8_t* q, int64_t ldq, const void* scales,
+                           const uint8_t* zeros, void* y);
+/* Quantise W [R, K] (finite) to that form, nearest in each group's grid: with
+ * zeros, scale = (max - min) / 15 over the group and 0; without, scale =
+ * max|w| / 7.  Scales are rounded to the handle's type first. */
+rnn_status_t rnn_w4_quantize(rnn_ops_t h, void* stream, int64_t R, int64_t K, int group,
+                             const void* W, uint8_t* q, int64_t ldq, void* scales, uint8_t* zeros);
+
 /* Static description of the status code. */
 const char* rnn_status_string(rnn_status_t s);
 

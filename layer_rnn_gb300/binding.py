@@ -70,6 +70,17 @@ SIGNATURES = {
                                     ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "rnn_debug_transpose_bf16": (_i32, [_vp, _i64, _i64, _i64, _vp, _i64, _vp]),
     "rnn_debug_wf_pack": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _pi64]),
+    "rnn_ops_create": (_i32, [ctypes.POINTER(_vp), _i32, _u32]),
+    "rnn_ops_destroy": (_i32, [_vp]),
+    "rnn_ops_check_status": (_i32, [_vp, _vp]),
+    "rnn_scan_workspace_size": (_i32, [_vp, _i64, _i64, _i64, _i32, _pi64]),
+    "rnn_scan_forward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _vp,
+                                _i64, _vp, _vp, _i64]),
+    "rnn_scan_backward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp,
+                                 _i64, _vp, _vp, _vp, _vp, _i64]),
+    "rnn_scan_step": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64]),
+    "rnn_w4_matvec": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp]),
+    "rnn_w4_quantize": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _vp]),
     "rnn_status_string": (ctypes.c_char_p, [_i32]),
 }
 
@@ -361,3 +372,141 @@ class Rnn:
 
     def check_status(self, stream=None):
         return rnn_check_status(self.h, self._stream(stream))
+
+
+class Ops:
+    """The sequence-block operators on torch tensors: one handle, one element
+    type.  Results go to the tensors that the caller gives; shapes, types and
+    devices are checked here, since the library only sees addresses.  Tensors
+    may be strided in the rows of ``gx``, ``dgx``, ``y`` and ``dy`` (as slices
+    of a wider buffer are); everything else is dense."""
+
+    def __init__(self, dtype="f32", flags=0):
+        import torch  # memory and streams only
+        self.torch = torch
+        self.dtype = dtype
+        self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.h = None
+        h = _vp()
+        _call("rnn_ops_create", ctypes.byref(h), DTYPES[dtype], flags)
+        self.h = h
+
+    def close(self):
+        if self.h is not None:
+            _call("rnn_ops_destroy", self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _stream(self, stream):
+        s = stream if stream is not None else self.torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def _check(self, name, t, shape, dtype=None):
+        """A dense tensor of this shape (or None): its address."""
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype != (dtype or self.tdtype):
+            raise ValueError("%s: expected %s %s, got %s %s" % (
+                name, tuple(shape), dtype or self.tdtype, tuple(t.shape), t.dtype))
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous CUDA tensor" % name)
+        return t.data_ptr()
+
+    def _rows(self, name, t, shape, pitch=None):
+        """A tensor [..., width] whose rows are evenly spaced: address, pitch."""
+        if t.shape != shape or t.dtype != self.tdtype or not t.is_cuda:
+            raise ValueError("%s: expected a CUDA tensor %s %s, got %s %s" % (
+                name, tuple(shape), self.tdtype, tuple(t.shape), t.dtype))
+        if t.is_contiguous():
+            ld = shape[-1]
+        else:
+            ld = t.stride(-2)
+            n = ld
+            for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+                if size > 1 and stride != n:
+                    raise ValueError("%s: rows are not evenly spaced" % name)
+                n *= size
+            if t.stride(-1) != 1:
+                raise ValueError("%s: the last dimension is not contiguous" % name)
+        if pitch is not None and ld != pitch:
+            raise ValueError("%s: row pitch %d, expected %d" % (name, ld, pitch))
+        return t.data_ptr(), ld
+
+    def check_status(self, stream=None):
+        return lib().rnn_ops_check_status(self.h, self._stream(stream))
+
+    # -- gated linear recurrence ------------------------------------------------
+    def scan_workspace_bytes(self, T, N, H, num_dirs=1):
+        b = ctypes.c_int64()
+        _call("rnn_scan_workspace_size", self.h, T, N, H, num_dirs, ctypes.byref(b))
+        return b.value
+
+    def scan_forward(self, gx, h0, y, hy, lengths=None, ws=None, out_gate=False, stream=None):
+        """gx [T, N, D*G*H], y [T, N, D*H], h0 and hy [D, N, H] (or None; one
+        of the two gives D, else D = 1)."""
+        T, N, width = gx.shape
+        G = 3 if out_gate else 2
+        D = h0.shape[0] if h0 is not None else hy.shape[0] if hy is not None else 1
+        H = width // (D * G)
+        f32 = self.torch.float32
+        pg, ldg = self._rows("gx", gx, (T, N, D * G * H))
+        py, ldy = self._rows("y", y, (T, N, D * H))
+        _call("rnn_scan_forward", self.h, self._stream(stream), T, N, H, D, int(out_gate),
+              self._check("lengths", lengths, (N,), self.torch.int32), pg, ldg,
+              self._check("h0", h0, (D, N, H), f32), py, ldy, self._check("hy", hy, (D, N, H), f32),
+              _p(ws), 0 if ws is None else ws.numel() * ws.element_size())
+
+    def scan_backward(self, gx, dy, dhy, dgx, dh0, ws, lengths=None, out_gate=False, stream=None):
+        T, N, width = gx.shape
+        G = 3 if out_gate else 2
+        D = dhy.shape[0] if dhy is not None else dh0.shape[0] if dh0 is not None else 1
+        H = width // (D * G)
+        f32 = self.torch.float32
+        pg, ldg = self._rows("gx", gx, (T, N, D * G * H))
+        pd, ldy = self._rows("dy", dy, (T, N, D * H))
+        _call("rnn_scan_backward", self.h, self._stream(stream), T, N, H, D, int(out_gate),
+              self._check("lengths", lengths, (N,), self.torch.int32), pg, ldg, pd, ldy,
+              self._check("dhy", dhy, (D, N, H), f32), self._rows("dgx", dgx, gx.shape, ldg)[0],
+              self._check("dh0", dh0, (D, N, H), f32), _p(ws), ws.numel() * ws.element_size())
+
+    def scan_step(self, gx, state, state_out, y, out_gate=False, stream=None):
+        """One token: gx [N, G*H], state and state_out [N, H] (may be the same
+        tensor), y [N, H]."""
+        N, H = state.shape
+        f32 = self.torch.float32
+        pg, ldg = self._rows("gx", gx, (N, (3 if out_gate else 2) * H))
+        py, ldy = self._rows("y", y, (N, H))
+        _call("rnn_scan_step", self.h, self._stream(stream), N, H, int(out_gate), pg, ldg,
+              self._check("state", state, (N, H), f32),
+              self._check("state_out", state_out, (N, H), f32), py, ldy)
+
+    # -- 4-bit weights ------------------------------------------------------------
+    def w4_alloc(self, R, K, group=128, zeros=False, device="cuda"):
+        """Empty (q, scales, zeros or None) for a weight [R, K]."""
+        t = self.torch
+        pitch, groups = ((K + 1) // 2 + 15) // 16 * 16, (K + group - 1) // group
+        return (t.empty((R, pitch), dtype=t.uint8, device=device),
+                t.empty((R, groups), dtype=self.tdtype, device=device),
+                t.empty((R, groups), dtype=t.uint8, device=device) if zeros else None)
+
+    def w4_quantize(self, W, q, scales, group=128, zeros=None, stream=None):
+        """W [R, K] to 4 bits, into the tensors of w4_alloc."""
+        R, K = W.shape
+        groups, u8 = (K + group - 1) // group, self.torch.uint8
+        _call("rnn_w4_quantize", self.h, self._stream(stream), R, K, group,
+              self._check("W", W, (R, K)), self._check("q", q, (R, q.shape[1]), u8), q.shape[1],
+              self._check("scales", scales, (R, groups)), self._check("zeros", zeros, (R, groups), u8))
+
+    def w4_matvec(self, x, q, scales, y, group=128, zeros=None, stream=None):
+        """y [M, R] = x [M, K] times the 4-bit weights [R, K] transposed."""
+        (M, K), R = x.shape, q.shape[0]
+        groups, u8 = (K + group - 1) // group, self.torch.uint8
+        _call("rnn_w4_matvec", self.h, self._stream(stream), M, R, K, group,
+              self._check("x", x, (M, K)), self._check("q", q, (R, q.shape[1]), u8), q.shape[1],
+              self._check("scales", scales, (R, groups)), self._check("zeros", zeros, (R, groups), u8),
+              self._check("y", y, (M, R)))

@@ -1,0 +1,255 @@
+// C ABI of the sequence-block operators: handle, argument checks and the
+// order of the kernels of each call.  See include/layer_rnn.h.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include "../../include/layer_rnn.h"
+#include "ops.h"
+
+using namespace lr;
+
+struct rnn_ops {
+  int dtype = 0;
+  uint32_t flags = 0;
+  // device state, set up by the first compute call
+  int device = -1;
+  int num_sms = 0;
+  int* d_status = nullptr;
+};
+
+namespace {
+
+constexpr int64_t kLimit = int64_t(1) << 31;
+
+int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
+bool on16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+template <typename... P>
+bool all_on16(const P*... p) {
+  return (on16(p) && ...);
+}
+
+rnn_status_t setup(rnn_ops* h) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RNN_ERR_CUDA;
+  if (h->device == dev && h->d_status) return RNN_OK;
+  if (h->device >= 0 && h->device != dev) return RNN_ERR_INVALID_ARG;  // one device per handle
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return RNN_ERR_CUDA;
+  void* p = nullptr;
+  if (cudaMalloc(&p, 256) != cudaSuccess) return RNN_ERR_CUDA;
+  if (cudaMemset(p, 0, 256) != cudaSuccess) {
+    cudaFree(p);
+    return RNN_ERR_CUDA;
+  }
+  h->d_status = static_cast<int*>(p);
+  h->device = dev;
+  h->num_sms = sms;
+  return RNN_OK;
+}
+
+rnn_status_t read_status(rnn_ops* h, cudaStream_t st) {
+  if (cudaStreamSynchronize(st) != cudaSuccess) return RNN_ERR_CUDA;
+  if (!h->d_status) return RNN_OK;
+  int v = 0;
+  if (cudaMemcpy(&v, h->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return RNN_ERR_CUDA;
+  if (v != 0 && cudaMemset(h->d_status, 0, sizeof(int)) != cudaSuccess) return RNN_ERR_CUDA;
+  return (rnn_status_t)v;
+}
+
+rnn_status_t finish(rnn_ops* h, cudaStream_t st, cudaError_t e) {
+  if (e != cudaSuccess) return RNN_ERR_CUDA;
+  if (h->flags & RNN_FLAG_SYNC_CHECK) return read_status(h, st);
+  return RNN_OK;
+}
+
+// sizes of a recurrence, and the pitches with their defaults filled in
+rnn_status_t scan_sizes(const rnn_ops* h, int64_t T, int64_t N, int64_t H, int D, int gate,
+                        int64_t* ldg, int64_t* ldy) {
+  if (!h || T < 1 || N < 1 || H < 1 || (D != 1 && D != 2) || (gate != 0 && gate != 1))
+    return RNN_ERR_INVALID_ARG;
+  if (T >= kLimit || N >= kLimit || H >= kLimit || N * D * H >= kLimit) return RNN_ERR_UNSUPPORTED;
+  const int64_t wg = D * (2 + gate) * H, wy = D * H;
+  if (*ldg == 0) *ldg = wg;
+  if (*ldy == 0) *ldy = wy;
+  if (*ldg < wg || *ldy < wy) return RNN_ERR_INVALID_ARG;
+  if (*ldg >= kLimit || *ldy >= kLimit) return RNN_ERR_UNSUPPORTED;
+  return RNN_OK;
+}
+
+int64_t scan_state_bytes(int64_t T, int64_t N, int64_t H, int D) {
+  return (T + kScanState - 1) / kScanState * N * D * H * 4;
+}
+
+ScanArgs scan_args(const rnn_ops* h, int64_t T, int64_t N, int64_t H, int D, int gate,
+                   const int32_t* lengths, const void* gx, int64_t ldg, int64_t ldy) {
+  ScanArgs a;
+  a.T = T; a.N = N; a.H = H; a.D = D;
+  a.gate = gate;
+  a.bf16 = h->dtype == RNN_BF16;
+  a.lengths = lengths;
+  a.gx = gx; a.ldg = ldg; a.ldy = ldy;
+  a.num_sms = h->num_sms;
+  return a;
+}
+
+rnn_status_t w4_args(const rnn_ops* h, int64_t M, int64_t R, int64_t K, int group, const uint8_t* q,
+                     int64_t ldq, const void* scales, const uint8_t* zeros, W4Args* a) {
+  if (!h || M < 1 || R < 1 || K < 1 || (group != 32 && group != 64 && group != 128) || !q || !scales)
+    return RNN_ERR_INVALID_ARG;
+  if (M >= kLimit || R >= kLimit || K > 65536) return RNN_ERR_UNSUPPORTED;
+  const int64_t row = (K + 1) / 2;
+  if (ldq == 0) ldq = (row + 15) / 16 * 16;
+  if (ldq < row || ldq % 16 != 0) return RNN_ERR_INVALID_ARG;
+  const bool bf = h->dtype == RNN_BF16;
+  if (!on16(q) || reinterpret_cast<uintptr_t>(scales) % (bf ? 2 : 4)) return RNN_ERR_MISALIGNED;
+  a->M = M; a->R = R; a->K = K; a->ldq = ldq;
+  a->group = group;
+  a->bf16 = bf;
+  a->q = q; a->scales = scales; a->zeros = zeros;
+  return RNN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rnn_status_t rnn_ops_create(rnn_ops_t* out, int dtype, uint32_t flags) {
+  if (!out) return RNN_ERR_INVALID_ARG;
+  *out = nullptr;
+  if ((dtype != RNN_F32 && dtype != RNN_BF16) || (flags & ~RNN_FLAG_SYNC_CHECK) != 0)
+    return RNN_ERR_INVALID_ARG;
+  rnn_ops* h = new (std::nothrow) rnn_ops();
+  if (!h) return RNN_ERR_INVALID_ARG;
+  h->dtype = dtype;
+  h->flags = flags;
+  *out = h;
+  return RNN_OK;
+}
+
+rnn_status_t rnn_ops_destroy(rnn_ops_t h) {
+  if (!h) return RNN_OK;
+  if (h->d_status) cudaFree(h->d_status);
+  delete h;
+  return RNN_OK;
+}
+
+rnn_status_t rnn_ops_check_status(rnn_ops_t h, void* stream) {
+  if (!h) return RNN_ERR_INVALID_ARG;
+  return read_status(h, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// gated linear recurrence
+// ---------------------------------------------------------------------------
+
+rnn_status_t rnn_scan_workspace_size(rnn_ops_t h, int64_t T, int64_t N, int64_t H, int num_dirs,
+                                     int64_t* bytes) {
+  int64_t ldg = 0, ldy = 0;
+  if (!bytes) return RNN_ERR_INVALID_ARG;
+  const rnn_status_t s = scan_sizes(h, T, N, H, num_dirs, 0, &ldg, &ldy);
+  if (s != RNN_OK) return s;
+  *bytes = round256(scan_state_bytes(T, N, H, num_dirs));
+  return RNN_OK;
+}
+
+rnn_status_t rnn_scan_forward(rnn_ops_t h, void* stream, int64_t T, int64_t N, int64_t H,
+                              int num_dirs, int out_gate, const int32_t* lengths, const void* gx,
+                              int64_t ldg, const float* h0, void* y, int64_t ldy, float* hy,
+                              void* workspace, int64_t ws_bytes) {
+  rnn_status_t s = scan_sizes(h, T, N, H, num_dirs, out_gate, &ldg, &ldy);
+  if (s != RNN_OK) return s;
+  if (!gx || !y) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(gx, y, h0, hy, workspace) || reinterpret_cast<uintptr_t>(lengths) % 4)
+    return RNN_ERR_MISALIGNED;
+  if (workspace && ws_bytes < scan_state_bytes(T, N, H, num_dirs))
+    return RNN_ERR_WORKSPACE_TOO_SMALL;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  ScanArgs a = scan_args(h, T, N, H, num_dirs, out_gate, lengths, gx, ldg, ldy);
+  a.h0 = h0;
+  a.y = y;
+  a.hy = hy;
+  a.states = static_cast<float*>(workspace);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, scan_forward(a, st));
+}
+
+rnn_status_t rnn_scan_backward(rnn_ops_t h, void* stream, int64_t T, int64_t N, int64_t H,
+                               int num_dirs, int out_gate, const int32_t* lengths, const void* gx,
+                               int64_t ldg, const void* dy, int64_t ldy, const float* dhy,
+                               void* dgx, float* dh0, const void* workspace, int64_t ws_bytes) {
+  rnn_status_t s = scan_sizes(h, T, N, H, num_dirs, out_gate, &ldg, &ldy);
+  if (s != RNN_OK) return s;
+  if (!gx || !dy || !dgx || !workspace) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(gx, dy, dhy, dgx, dh0, workspace) || reinterpret_cast<uintptr_t>(lengths) % 4)
+    return RNN_ERR_MISALIGNED;
+  if (ws_bytes < scan_state_bytes(T, N, H, num_dirs)) return RNN_ERR_WORKSPACE_TOO_SMALL;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  ScanArgs a = scan_args(h, T, N, H, num_dirs, out_gate, lengths, gx, ldg, ldy);
+  a.dy = dy;
+  a.dhy = dhy;
+  a.dgx = dgx;
+  a.dh0 = dh0;
+  a.states = static_cast<float*>(const_cast<void*>(workspace));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, scan_backward(a, st));
+}
+
+rnn_status_t rnn_scan_step(rnn_ops_t h, void* stream, int64_t N, int64_t H, int out_gate,
+                           const void* gx, int64_t ldg, const float* state, float* state_out,
+                           void* y, int64_t ldy) {
+  rnn_status_t s = scan_sizes(h, 1, N, H, 1, out_gate, &ldg, &ldy);
+  if (s != RNN_OK) return s;
+  if (!gx || !state || !state_out || !y) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(gx, state, state_out, y)) return RNN_ERR_MISALIGNED;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  ScanArgs a = scan_args(h, 1, N, H, 1, out_gate, nullptr, gx, ldg, ldy);
+  a.h0 = state;
+  a.y = y;
+  a.hy = state_out;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, scan_forward(a, st));
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit weights
+// ---------------------------------------------------------------------------
+
+rnn_status_t rnn_w4_matvec(rnn_ops_t h, void* stream, int64_t M, int64_t R, int64_t K, int group,
+                           const void* x, const uint8_t* q, int64_t ldq, const void* scales,
+                           const uint8_t* zeros, void* y) {
+  W4Args a;
+  rnn_status_t s = w4_args(h, M, R, K, group, q, ldq, scales, zeros, &a);
+  if (s != RNN_OK) return s;
+  if (!x || !y) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(x, y)) return RNN_ERR_MISALIGNED;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  a.x = x;
+  a.y = y;
+  a.num_sms = h->num_sms;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, w4_matvec(a, st));
+}
+
+rnn_status_t rnn_w4_quantize(rnn_ops_t h, void* stream, int64_t R, int64_t K, int group,
+                             const void* W, uint8_t* q, int64_t ldq, void* scales, uint8_t* zeros) {
+  W4Args a;
+  rnn_status_t s = w4_args(h, 1, R, K, group, q, ldq, scales, zeros, &a);
+  if (s != RNN_OK) return s;
+  if (!W) return RNN_ERR_INVALID_ARG;
+  if (!on16(W)) return RNN_ERR_MISALIGNED;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  a.num_sms = h->num_sms;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, w4_quantize(a, W, st));
+}
+
+}  // extern "C"

@@ -1,0 +1,50 @@
+// Host-side declarations of the sequence-block operators (scan.cu, glu*.cu,
+// w4.cu) for their API layer (api_ops.cu).
+#pragma once
+
+#include "host_common.h"
+
+namespace lr {
+
+// ---------------------------------------------------------------------------
+// gated linear recurrence
+// ---------------------------------------------------------------------------
+constexpr int kScanState = 64;  // steps between the states that training saves
+
+struct ScanArgs {
+  int64_t T = 0, N = 0, H = 0, D = 1;
+  int gate = 0;                       // third block: output gate
+  int bf16 = 0;
+  const int* lengths = nullptr;       // [N] or null
+  const void* gx = nullptr; int64_t ldg = 0;
+  const float* h0 = nullptr;          // [D, N, H] or null (zeros)
+  void* y = nullptr; int64_t ldy = 0;
+  float* hy = nullptr;                // [D, N, H] or null
+  float* states = nullptr;            // training: [ceil(T / kScanState)][N, D, H]
+  // backward
+  const void* dy = nullptr;           // row pitch ldy
+  const float* dhy = nullptr;
+  void* dgx = nullptr;                // row pitch ldg
+  float* dh0 = nullptr;
+  int num_sms = 0;
+};
+cudaError_t scan_forward(const ScanArgs& a, cudaStream_t st);
+cudaError_t scan_backward(const ScanArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------------------
+// 4-bit weights
+// ---------------------------------------------------------------------------
+struct W4Args {
+  int64_t M = 0, R = 0, K = 0, ldq = 0;  // ldq: bytes of a row of q
+  int group = 0, bf16 = 0;
+  const void* x = nullptr;
+  const uint8_t* q = nullptr;
+  const void* scales = nullptr;          // [R][ceil(K / group)]
+  const uint8_t* zeros = nullptr;        // the same shape, or null (8 everywhere)
+  void* y = nullptr;
+  int num_sms = 0;
+};
+cudaError_t w4_matvec(const W4Args& a, cudaStream_t st);
+cudaError_t w4_quantize(const W4Args& a, const void* w, cudaStream_t st);
+
+}  // namespace lr
