@@ -455,6 +455,28 @@ rnn_status_t rnn_scan_step(rnn_ops_t h, void* stream, int64_t N, int64_t H, int 
                            const void* gx, int64_t ldg, const float* state, float* state_out,
                            void* y, int64_t ldy);
 
+/* ---- gated feed-forward ----
+ * y = act(x Wg^T) * (x Wu^T): both projections, the activation and the product.
+ * x [M, K], W [2F, K] (the F gate rows, then the F up rows), y [M, F]; act:
+ * rnn_act_t.  M = 1 (a token) and up; any K and F.
+ * Backward: dx [M, K] and dW [2F, K] (overwritten; either may be NULL) of
+ * sum(y*dy).  It computes the pre-activations again, so nothing but x and W is
+ * kept from the forward.  RNN_BF16 rounds dg and du, the gradients of the
+ * pre-activations, to bfloat16 between its products.
+ * workspace: scratch of the call, rnn_glu_workspace_size bytes (backward 0 or
+ * 1; the backward's serves both), 256-byte aligned; nothing is kept in it.
+ * Errors: RNN_ERR_INVALID_ARG, RNN_ERR_MISALIGNED, RNN_ERR_WORKSPACE_TOO_SMALL;
+ * RNN_ERR_UNSUPPORTED for M, K or 2F of 2^24 and more. */
+typedef enum { RNN_ACT_SILU = 0, RNN_ACT_GELU_TANH = 1, RNN_ACT_SIGMOID = 2 } rnn_act_t;
+rnn_status_t rnn_glu_workspace_size(rnn_ops_t h, int64_t M, int64_t K, int64_t F, int backward,
+                                    int64_t* bytes);
+rnn_status_t rnn_glu_forward(rnn_ops_t h, void* stream, int64_t M, int64_t K, int64_t F, int act,
+                             const void* x, const void* W, void* y, void* workspace,
+                             int64_t ws_bytes);
+rnn_status_t rnn_glu_backward(rnn_ops_t h, void* stream, int64_t M, int64_t K, int64_t F, int act,
+                              const void* x, const void* W, const void* dy, void* dx, void* dW,
+                              void* workspace, int64_t ws_bytes);
+
 /* ---- matrix-vector products with 4-bit weights ----
  * y[m][r] = sum_k x[m][k] (q[r][k] - zero[r][k / group]) scale[r][k / group]
  * x [M, K], y [M, R]; q: R rows of ldq bytes, weight k in the low (even k) or

@@ -27,6 +27,8 @@ STATUS = {0: "RNN_OK", 1: "RNN_ERR_INVALID_ARG", 2: "RNN_ERR_UNSUPPORTED",
           6: "RNN_ERR_TIMEOUT", 7: "RNN_ERR_NO_RESIDENCY", 8: "RNN_ERR_DEVICE_CHECK"}
 MODES = {"rnn_tanh": RNN_TANH, "lstm": RNN_LSTM, "gru": RNN_GRU, "gru_tf": RNN_GRU_TF}
 DTYPES = {"f32": RNN_F32, "bf16": RNN_BF16}
+RNN_ACT_SILU, RNN_ACT_GELU_TANH, RNN_ACT_SIGMOID = range(3)
+ACTS = {"silu": RNN_ACT_SILU, "gelu": RNN_ACT_GELU_TANH, "sigmoid": RNN_ACT_SIGMOID}
 
 # exported symbol -> (restype, argtypes)
 _i64, _i32, _u32, _vp = ctypes.c_int64, ctypes.c_int, ctypes.c_uint32, ctypes.c_void_p
@@ -79,6 +81,10 @@ SIGNATURES = {
     "rnn_scan_backward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _i64, _vp,
                                  _i64, _vp, _vp, _vp, _vp, _i64]),
     "rnn_scan_step": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64]),
+    "rnn_glu_workspace_size": (_i32, [_vp, _i64, _i64, _i64, _i32, _pi64]),
+    "rnn_glu_forward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64]),
+    "rnn_glu_backward": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _i64]),
     "rnn_w4_matvec": (_i32, [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _vp, _vp]),
     "rnn_w4_quantize": (_i32, [_vp, _vp, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _vp]),
     "rnn_status_string": (ctypes.c_char_p, [_i32]),
@@ -484,6 +490,27 @@ class Ops:
         _call("rnn_scan_step", self.h, self._stream(stream), N, H, int(out_gate), pg, ldg,
               self._check("state", state, (N, H), f32),
               self._check("state_out", state_out, (N, H), f32), py, ldy)
+
+    # -- gated feed-forward -------------------------------------------------------
+    def glu_workspace_bytes(self, M, K, F, backward=False):
+        b = ctypes.c_int64()
+        _call("rnn_glu_workspace_size", self.h, M, K, F, int(backward), ctypes.byref(b))
+        return b.value
+
+    def glu_forward(self, x, W, y, ws, act="silu", stream=None):
+        """y [M, F] = act(x Wg^T) * (x Wu^T), x [M, K], W = [Wg; Wu] [2F, K]."""
+        (M, K), F = x.shape, W.shape[0] // 2
+        _call("rnn_glu_forward", self.h, self._stream(stream), M, K, F, ACTS[act],
+              self._check("x", x, (M, K)), self._check("W", W, (2 * F, K)),
+              self._check("y", y, (M, F)), _p(ws), ws.numel() * ws.element_size())
+
+    def glu_backward(self, x, W, dy, dx, dW, ws, act="silu", stream=None):
+        """dx [M, K] and dW [2F, K] (either may be None)."""
+        (M, K), F = x.shape, W.shape[0] // 2
+        _call("rnn_glu_backward", self.h, self._stream(stream), M, K, F, ACTS[act],
+              self._check("x", x, (M, K)), self._check("W", W, (2 * F, K)),
+              self._check("dy", dy, (M, F)), self._check("dx", dx, (M, K)),
+              self._check("dW", dW, (2 * F, K)), _p(ws), ws.numel() * ws.element_size())
 
     # -- 4-bit weights ------------------------------------------------------------
     def w4_alloc(self, R, K, group=128, zeros=False, device="cuda"):

@@ -113,6 +113,35 @@ rnn_status_t w4_args(const rnn_ops* h, int64_t M, int64_t R, int64_t K, int grou
   return RNN_OK;
 }
 
+rnn_status_t glu_sizes(const rnn_ops* h, int64_t M, int64_t K, int64_t F) {
+  if (!h || M < 1 || K < 1 || F < 1) return RNN_ERR_INVALID_ARG;
+  const int64_t most = int64_t(1) << 24;
+  if (M >= most || K >= most || 2 * F >= most) return RNN_ERR_UNSUPPORTED;
+  return RNN_OK;
+}
+
+// rows up to which the forward streams W past the tokens (see glu_rows.cu)
+bool glu_few(const rnn_ops* h, int64_t M) { return M <= (h->dtype == RNN_BF16 ? 32 : 64); }
+
+int64_t glu_workspace(const rnn_ops* h, int64_t M, int64_t K, int64_t F, bool backward) {
+  if (!backward && glu_few(h, M)) return 256;
+  return h->dtype == RNN_BF16 ? glu_tc_workspace(M, K, F, backward)
+                              : glu_f32_workspace(M, K, F, backward);
+}
+
+rnn_status_t glu_args(rnn_ops* h, int64_t M, int64_t K, int64_t F, int act, const void* x,
+                      const void* W, void* ws, int64_t ws_bytes, bool backward, GluArgs* a) {
+  if (act < RNN_ACT_SILU || act > RNN_ACT_SIGMOID || !x || !W || !ws) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(x, W) || reinterpret_cast<uintptr_t>(ws) % 256) return RNN_ERR_MISALIGNED;
+  if (ws_bytes < glu_workspace(h, M, K, F, backward)) return RNN_ERR_WORKSPACE_TOO_SMALL;
+  a->M = M; a->K = K; a->F = F;
+  a->act = act;
+  a->bf16 = h->dtype == RNN_BF16;
+  a->x = x; a->W = W;
+  a->workspace = ws;
+  return RNN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,6 +244,59 @@ rnn_status_t rnn_scan_step(rnn_ops_t h, void* stream, int64_t N, int64_t H, int 
   a.hy = state_out;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return finish(h, st, scan_forward(a, st));
+}
+
+// ---------------------------------------------------------------------------
+// gated feed-forward
+// ---------------------------------------------------------------------------
+
+rnn_status_t rnn_glu_workspace_size(rnn_ops_t h, int64_t M, int64_t K, int64_t F, int backward,
+                                    int64_t* bytes) {
+  if (!bytes || (backward != 0 && backward != 1)) return RNN_ERR_INVALID_ARG;
+  const rnn_status_t s = glu_sizes(h, M, K, F);
+  if (s != RNN_OK) return s;
+  *bytes = glu_workspace(h, M, K, F, backward != 0);
+  return RNN_OK;
+}
+
+rnn_status_t rnn_glu_forward(rnn_ops_t h, void* stream, int64_t M, int64_t K, int64_t F, int act,
+                             const void* x, const void* W, void* y, void* workspace,
+                             int64_t ws_bytes) {
+  GluArgs a;
+  rnn_status_t s = glu_sizes(h, M, K, F);
+  if (s == RNN_OK) s = glu_args(h, M, K, F, act, x, W, workspace, ws_bytes, false, &a);
+  if (s != RNN_OK) return s;
+  if (!y) return RNN_ERR_INVALID_ARG;
+  if (!on16(y)) return RNN_ERR_MISALIGNED;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  a.y = y;
+  a.num_sms = h->num_sms;
+  a.status = h->d_status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, glu_few(h, M) ? glu_rows_forward(a, st)
+                       : a.bf16      ? glu_tc_forward(a, st)
+                                     : glu_f32_forward(a, st));
+}
+
+rnn_status_t rnn_glu_backward(rnn_ops_t h, void* stream, int64_t M, int64_t K, int64_t F, int act,
+                              const void* x, const void* W, const void* dy, void* dx, void* dW,
+                              void* workspace, int64_t ws_bytes) {
+  GluArgs a;
+  rnn_status_t s = glu_sizes(h, M, K, F);
+  if (s == RNN_OK) s = glu_args(h, M, K, F, act, x, W, workspace, ws_bytes, true, &a);
+  if (s != RNN_OK) return s;
+  if (!dy || (!dx && !dW)) return RNN_ERR_INVALID_ARG;
+  if (!all_on16(dy, dx, dW)) return RNN_ERR_MISALIGNED;
+  s = setup(h);
+  if (s != RNN_OK) return s;
+  a.dy = dy;
+  a.dx = dx;
+  a.dW = dW;
+  a.num_sms = h->num_sms;
+  a.status = h->d_status;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return finish(h, st, a.bf16 ? glu_tc_backward(a, st) : glu_f32_backward(a, st));
 }
 
 // ---------------------------------------------------------------------------

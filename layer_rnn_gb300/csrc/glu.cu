@@ -1,0 +1,509 @@
+// Gated feed-forward, bfloat16, on the tensor cores.
+//
+//   y = act(x Wg^T) * (x Wu^T),   W = [Wg; Wu] [2F][K]
+//
+// One persistent kernel for four products.  Two blocks (a cluster) work on a
+// 256 x 256 tile of the result with one tcgen05.mma of M = N = 256: each loads
+// half of either operand by TMA, so an operand byte is fetched into shared
+// memory once for 256 rows or columns.  Two accumulators in tensor memory
+// (512 columns) let eight epilogue warps finish a tile while the next one is
+// multiplied.
+//
+//   forward   columns 0..127 of a tile are gate rows of W (loaded by block 0),
+//             128..255 the up rows of the same features (block 1): both
+//             pre-activations of an output meet in one thread, which applies
+//             the activation and the product in float32 and rounds once
+//   dgu       the same product again, not kept from the forward pass, with
+//             dg = dy u act'(g), du = dy act(g) as epilogue.  Computing it
+//             again costs a third of the backward pass's arithmetic and saves
+//             4 MF bytes kept by every layer; g and u stay float32
+//   dx        dg Wg + du Wu: the contraction runs over two planes
+//   dW        [dg du]^T x
+//
+// dgu is rounded to bfloat16 (the operand type).  The operands of dx and dW
+// that are contiguous along the result (W, dgu, x) are read as they are, through
+// MN-major shared-memory descriptors: no transposed copies.
+//
+// dx and dW have few tiles and long contractions: tiles that do not fill a
+// last round are cut evenly along the contraction over all pairs of blocks,
+// their partial sums kept in float32 and joined in a fixed order.
+//
+// Bound by the tensor cores: 4 M K F flop forward against 2 (MK + 2FK + MF)
+// bytes.  Every wait is bounded by %globaltimer.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "glu_tc.cuh"
+#include "ops.h"
+
+namespace lr {
+namespace {
+
+using namespace glu;
+
+constexpr int kTile = 256;                 // rows and columns of a pair's tile
+constexpr int kOperand = kHalf * 128;      // bytes of half an operand, 64 elements of k
+constexpr int kStage = 2 * kOperand;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBox = 32 * 128;             // 32 rows of 64 bf16
+constexpr int kSmem = 231424;              // dynamic shared memory of a block
+
+struct Maps {
+  CUtensorMap a, b, out, dy;
+};
+
+template <int PROD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    glu_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  constexpr bool kAmn = PROD == kDw, kBmn = PROD == kDx || PROD == kDw;
+  constexpr bool kGated = PROD == kForward || PROD == kDgu;
+  constexpr int kBoxes = PROD == kDgu ? 2 : 1;  // staging boxes of an epilogue warp
+  constexpr int ST = (kSmem - 1024 - kEpiWarps * kBoxes * kBox) / kStage;
+  // kind::f16, bf16 operands, float32 sums, M = 256, N = 256
+  constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kAmn ? 1u : 0u) << 15) |
+                              ((kBmn ? 1u : 0u) << 16) | ((uint32_t)(kTile >> 3) << 17) |
+                              ((uint32_t)(kTile >> 4) << 24);
+  __shared__ __align__(8) uint64_t bars[2 * ST + 4 + kEpiWarps];
+  __shared__ uint32_t tmem_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = tc::cl_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t full0 = tc::smem_addr(&bars[0]), empty0 = full0 + 8 * ST;
+  const uint32_t tfull0 = empty0 + 8 * ST, tempty0 = tfull0 + 16, dy0 = tempty0 + 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      tc::mbar_init(full0 + 8 * s, 1);   // block 0's: its own arrival and both blocks' bytes
+      tc::mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tfull0 + 8 * i, 1);
+      tc::mbar_init(tempty0 + 8 * i, 2 * kEpiWarps);  // block 0's
+    }
+    for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(dy0 + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_addr(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cl_sync();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  Walk w;
+  walk_start(p, w, pair, pairs);
+  if (threadIdx.x == 0) {
+    // loads, in both blocks
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    while (ok && walk_next(p, w, pairs)) {
+      int z, mt, nt;
+      tile_at(p, w.tile, z, mt, nt);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (!tc::mbar_wait_cluster_bounded(empty0 + 8 * s, ph, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a = base + (uint32_t)(s * kStage), b = a + kOperand;
+        if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStage);
+        const uint32_t bar = map_rank(full0 + 8 * s, 0);
+        if (kGated) {
+          load_box(a, &maps.a, kb * 64, mt * kTile + (int)rank * kHalf, 0, bar);
+          load_box(b, &maps.b, kb * 64, nt * kHalf, (int)rank, bar);
+        } else if (PROD == kDx) {
+          const int pl = kb >= p.kb_plane, k = (kb - pl * p.kb_plane) * 64;
+          load_box(a, &maps.a, k, mt * kTile + (int)rank * kHalf, pl, bar);
+          const int n0 = nt * kTile + (int)rank * kHalf;
+          load_box(b, &maps.b, n0, k, pl, bar);
+          load_box(b + 8192, &maps.b, n0 + 64, k, pl, bar);
+        } else {
+          const int f0 = mt * kTile + (int)rank * kHalf, n0 = nt * kTile + (int)rank * kHalf;
+          load_box(a, &maps.a, f0, kb * 64, z, bar);
+          load_box(a + 8192, &maps.a, f0 + 64, kb * 64, z, bar);
+          load_box(b, &maps.b, n0, kb * 64, 0, bar);
+          load_box(b + 8192, &maps.b, n0 + 64, kb * 64, 0, bar);
+        }
+        if (++s == ST) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok) {
+      // copies in flight land within microseconds: stay that long
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (threadIdx.x == 32 && rank == 0) {
+    // MMAs, for both blocks
+    int s = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    while (ok && walk_next(p, w, pairs)) {
+      const int buf = n & 1;
+      if (!tc::mbar_wait_cluster_bounded(tempty0 + 8 * buf, ((n >> 1) & 1) ^ 1u, p.status,
+                                         p.timeout_ns))
+        break;
+      tc::fence_after();
+      const uint32_t d = tmem + (uint32_t)(buf * 256);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (!tc::mbar_wait_cluster_bounded(full0 + 8 * s, ph, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t a = base + (uint32_t)(s * kStage);
+        const uint64_t ad = operand_desc<kAmn>(a), bd = operand_desc<kBmn>(a + kOperand);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma2(d, ad + (uint64_t)(kk * (kAmn ? 128 : 2)), bd + (uint64_t)(kk * (kBmn ? 128 : 2)),
+               kIdesc, (kb > w.kb0 || kk > 0) ? 1u : 0u);
+        commit2(empty0 + 8 * s);
+        if (++s == ST) { s = 0; ph ^= 1u; }
+      }
+      if (ok) commit2(tfull0 + 8 * buf);
+      ++n;
+    }
+  } else if (warp >= 2) {
+    // epilogue: warp e takes lanes (rows) 32 (warp % 4) and half e / 4 of the
+    // columns (of the features, where gate and up columns belong together)
+    const int e = warp - 2, q = warp & 3, half = e >> 2;
+    const uint32_t box0 = base + (uint32_t)(ST * kStage + e * kBoxes * kBox);
+    const uint32_t tempty = map_rank(tempty0, 0);
+    uint32_t dy_ph = 0;
+    int n = 0;
+    while (walk_next(p, w, pairs)) {
+      int z, mt, nt;
+      tile_at(p, w.tile, z, mt, nt);
+      const int buf = n & 1;
+      const int row0 = mt * kTile + (int)rank * kHalf + q * 32;
+      const uint32_t lanes = tmem + (uint32_t)(buf * 256) + ((uint32_t)(q * 32) << 16);
+      const int f0 = nt * kHalf + half * 64;  // first feature of a gated tile
+      if (PROD == kDgu && p.tma_dy) {
+        // dy under the product: its box is free once du, stored from it, has been read
+        if (lane == 0) {
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          tc::mbar_arrive_expect_tx(dy0 + 8 * e, kBox);
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+              " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box0 + kBox),
+              "l"(reinterpret_cast<uint64_t>(&maps.dy)), "r"(f0), "r"(row0), "r"(0),
+              "r"(dy0 + 8 * e)
+              : "memory");
+        }
+        __syncwarp();
+      }
+      if (!__all_sync(0xffffffffu, tc::mbar_wait_cluster_bounded(tfull0 + 8 * buf, (n >> 1) & 1,
+                                                                 p.status, p.timeout_ns)))
+        break;
+      tc::fence_after();
+      ++n;
+      if (w.partial) {
+        // float32, 32 lanes x 4 columns a store, in the order the reduction reads
+        float4* d = part_at<kTile>(p, pair, w.slot, (int)rank * 4 + q) + lane;
+#pragma unroll 1
+        for (int c = half * 128; c < half * 128 + 128; c += 32) {
+          float v[32];
+          tc::tmem_ld32(lanes + (uint32_t)c, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcs(d + (c / 4 + i) * 32, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(tempty + 8 * buf);
+        continue;
+      }
+      if (kGated) {
+        if (PROD == kDgu && p.tma_dy) {
+          if (!__all_sync(0xffffffffu,
+                          tc::mbar_wait_bounded(dy0 + 8 * e, dy_ph, p.status, p.timeout_ns)))
+            break;
+          dy_ph ^= 1u;
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        const uint32_t row_at = box0 + (uint32_t)lane * 128u;
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          float g[32], u[32];
+          tc::tmem_ld32(lanes + (uint32_t)(half * 64 + c), g);
+          tc::tmem_ld32(lanes + (uint32_t)(128 + half * 64 + c), u);
+          if (c == 32) {  // the accumulator has been read
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(tempty + 8 * buf);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t piece = (uint32_t)(((c >> 3) + j) ^ (lane & 7)) << 4;
+            uint32_t o[4], o2[4];
+            uint4 dv = make_uint4(0, 0, 0, 0);
+            if (PROD == kDgu) {
+              if (p.tma_dy) {
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(dv.x), "=r"(dv.y), "=r"(dv.z), "=r"(dv.w)
+                             : "r"(row_at + kBox + piece));
+              } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int f = f0 + c + 8 * j + i;
+                  h[i] = row0 + lane < p.rows && f < p.cols
+                             ? static_cast<const unsigned short*>(p.dy)[(int64_t)(row0 + lane) * p.ld_dy + f]
+                             : 0u;
+                }
+                dv = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int k = 8 * j + 2 * i;
+              if (PROD == kForward) {
+                o[i] = glu::pack2(glu::value(g[k], p.act) * u[k], glu::value(g[k + 1], p.act) * u[k + 1]);
+              } else {
+                const uint32_t dw = i == 0 ? dv.x : i == 1 ? dv.y : i == 2 ? dv.z : dv.w;
+                const float y0 = __uint_as_float(dw << 16), y1 = __uint_as_float(dw & 0xffff0000u);
+                float v0, d0, v1, d1;
+                glu::value_slope(g[k], p.act, v0, d0);
+                glu::value_slope(g[k + 1], p.act, v1, d1);
+                o[i] = glu::pack2(y0 * u[k] * d0, y1 * u[k + 1] * d1);
+                o2[i] = glu::pack2(y0 * v0, y1 * v1);
+              }
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + piece), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+            if (PROD == kDgu)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + kBox + piece),
+                           "r"(o2[0]), "r"(o2[1]), "r"(o2[2]), "r"(o2[3])
+                           : "memory");
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (p.tma_out) {
+          if (lane == 0 && row0 < p.rows && f0 < p.cols) {
+            store_box(&maps.out, box0, f0, row0, 0);
+            if (PROD == kDgu) store_box(&maps.out, box0 + kBox, f0, row0, 1);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          glu::store_rows(box0, static_cast<bf16*>(p.out), p.ld_out, row0, f0, p.rows, p.cols, lane);
+        }
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int c0 = half * 128; c0 < half * 128 + 128; c0 += 64) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+          const uint32_t row_at = box0 + (uint32_t)lane * 128u;
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float v[32];
+            tc::tmem_ld32(lanes + (uint32_t)(c0 + c), v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t piece = (uint32_t)(((c >> 3) + j) ^ (lane & 7)) << 4;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + piece),
+                           "r"(glu::pack2(v[8 * j], v[8 * j + 1])), "r"(glu::pack2(v[8 * j + 2], v[8 * j + 3])),
+                           "r"(glu::pack2(v[8 * j + 4], v[8 * j + 5])), "r"(glu::pack2(v[8 * j + 6], v[8 * j + 7]))
+                           : "memory");
+            }
+          }
+          if (c0 == half * 128 + 64) {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(tempty + 8 * buf);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          const int col0 = nt * kTile + c0;
+          if (p.tma_out) {
+            if (lane == 0 && row0 < p.rows && col0 < p.cols) {
+              store_box(&maps.out, box0, col0, row0, z);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          } else {
+            glu::store_rows(box0, static_cast<bf16*>(p.out) + (int64_t)z * p.rows * p.ld_out, p.ld_out, row0, col0,
+                            p.rows, p.cols, lane);
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::cl_sync();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+// rows of `cols` bf16 to rows of pitch ldd (a multiple of 8), so that TMA can
+// read them
+__global__ void __launch_bounds__(256) pad_rows_kernel(const unsigned short* __restrict__ src,
+                                                       int64_t rows, int cols,
+                                                       unsigned short* dst, int ldd) {
+  const int64_t total = rows * ldd;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / ldd;
+    const int c = (int)(i - r * ldd);
+    dst[i] = c < cols ? src[r * cols + c] : (unsigned short)0;
+  }
+}
+
+template <int PROD>
+cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+  auto kernel = glu_gemm_kernel<PROD>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = plan_pairs(&p, a.num_sms, 24);  // 256 KB each way
+  // few row tiles walked together keep their rows of A in L2 beside all of B
+  p.group = std::min(p.m_tiles, 16);
+  p.status = a.status;
+  p.timeout_ns = 2000000000LL;
+  kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  e = cudaGetLastError();
+  const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
+  if (e != cudaSuccess || cut_tiles == 0) return e;
+  glu_join_kernel<bf16, kTile><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError();
+}
+
+// x and W with rows that TMA can read: as they are, or copied
+struct Operands {
+  const void* x;
+  const void* W;
+  int64_t ld;
+};
+cudaError_t operands(const GluArgs& a, char** ws, Operands* o, bool copy, cudaStream_t st) {
+  o->x = a.x; o->W = a.W; o->ld = a.K;
+  if (a.K % 8 == 0) return cudaSuccess;
+  o->ld = pad8(a.K);
+  char* xc = *ws;
+  char* wc = xc + round256(a.M * o->ld * 2);
+  *ws = wc + round256(2 * a.F * o->ld * 2);
+  o->x = xc; o->W = wc;
+  if (!copy) return cudaSuccess;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t rows = i ? 2 * a.F : a.M;
+    const int blocks = (int)std::min<int64_t>(ceil_div(rows * o->ld, 256), (int64_t)a.num_sms * 16);
+    pad_rows_kernel<<<blocks, 256, 0, st>>>(static_cast<const unsigned short*>(i ? a.W : a.x), rows,
+                                            (int)a.K, reinterpret_cast<unsigned short*>(i ? wc : xc),
+                                            (int)o->ld);
+    g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t glu_tc_workspace(int64_t M, int64_t K, int64_t F, bool backward) {
+  int64_t b = 256;
+  if (K % 8) b += round256(M * pad8(K) * 2) + round256(2 * F * pad8(K) * 2);
+  if (!backward) return b;
+  b += round256(2 * M * pad8(F) * 2);
+  return b + (int64_t)kGluMaxPairs * 2 * kTile * kTile * 4;
+}
+
+cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st) {
+  char* ws = static_cast<char*>(a.workspace);
+  Operands o;
+  cudaError_t e = operands(a, &ws, &o, true, st);
+  if (e != cudaSuccess) return e;
+  Maps maps = {};
+  P p = {};
+  if (!map3(&maps.a, o.x, a.K, a.M, 1, o.ld, a.M, 128) ||
+      !map3(&maps.b, o.W, a.K, a.F, 2, o.ld, a.F, 128))
+    return cudaErrorInvalidValue;
+  p.tma_out = a.F % 8 == 0 && map3(&maps.out, a.y, a.F, a.M, 1, a.F, a.M, 32);
+  p.m_tiles = (int)ceil_div(a.M, kTile);
+  p.n_tiles = (int)ceil_div(a.F, kHalf);
+  p.planes = 1;
+  p.nkb = (int)ceil_div(a.K, 64);
+  p.rows = (int)a.M; p.cols = (int)a.F;
+  p.act = a.act;
+  p.out = a.y; p.ld_out = a.F;
+  return launch<kForward>(maps, p, a, st);
+}
+
+cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
+  char* ws = static_cast<char*>(a.workspace);
+  Operands o;
+  cudaError_t e = operands(a, &ws, &o, true, st);
+  if (e != cudaSuccess) return e;
+  const int64_t Fp = pad8(a.F);
+  char* dgu = ws;
+  float* part = reinterpret_cast<float*>(ws + round256(2 * a.M * Fp * 2));
+  {
+    Maps maps = {};
+    P p = {};
+    if (!map3(&maps.a, o.x, a.K, a.M, 1, o.ld, a.M, 128) ||
+        !map3(&maps.b, o.W, a.K, a.F, 2, o.ld, a.F, 128) ||
+        !map3(&maps.out, dgu, a.F, a.M, 2, Fp, a.M, 32))
+      return cudaErrorInvalidValue;
+    p.tma_out = 1;
+    p.tma_dy = a.F % 8 == 0 && map3(&maps.dy, a.dy, a.F, a.M, 1, a.F, a.M, 32);
+    p.m_tiles = (int)ceil_div(a.M, kTile);
+    p.n_tiles = (int)ceil_div(a.F, kHalf);
+    p.planes = 1;
+    p.nkb = (int)ceil_div(a.K, 64);
+    p.rows = (int)a.M; p.cols = (int)a.F;
+    p.act = a.act;
+    p.dy = a.dy; p.ld_dy = a.F;
+    e = launch<kDgu>(maps, p, a, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dx) {
+    Maps maps = {};
+    P p = {};
+    if (!map3(&maps.a, dgu, a.F, a.M, 2, Fp, a.M, 128) ||
+        !map3(&maps.b, o.W, a.K, a.F, 2, o.ld, a.F, 64))
+      return cudaErrorInvalidValue;
+    p.tma_out = a.K % 8 == 0 && map3(&maps.out, a.dx, a.K, a.M, 1, a.K, a.M, 32);
+    p.m_tiles = (int)ceil_div(a.M, kTile);
+    p.n_tiles = (int)ceil_div(a.K, kTile);
+    p.planes = 1;
+    p.kb_plane = (int)ceil_div(a.F, 64);
+    p.nkb = 2 * p.kb_plane;
+    p.rows = (int)a.M; p.cols = (int)a.K;
+    p.out = a.dx; p.ld_out = a.K;
+    p.part = part;
+    e = launch<kDx>(maps, p, a, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dW) {
+    Maps maps = {};
+    P p = {};
+    if (!map3(&maps.a, dgu, a.F, a.M, 2, Fp, a.M, 64) ||
+        !map3(&maps.b, o.x, a.K, a.M, 1, o.ld, a.M, 64))
+      return cudaErrorInvalidValue;
+    p.tma_out = a.K % 8 == 0 && map3(&maps.out, a.dW, a.K, a.F, 2, a.K, a.F, 32);
+    p.m_tiles = (int)ceil_div(a.F, kTile);
+    p.n_tiles = (int)ceil_div(a.K, kTile);
+    p.planes = 2;
+    p.nkb = (int)ceil_div(a.M, 64);
+    p.rows = (int)a.F; p.cols = (int)a.K;
+    p.out = a.dW; p.ld_out = a.K;
+    p.part = part;
+    e = launch<kDw>(maps, p, a, st);
+  }
+  return e;
+}
+
+}  // namespace lr

@@ -1,0 +1,61 @@
+// Device helpers of the gated feed-forward kernels: the activations and the
+// rounding and storing of their results.
+#pragma once
+
+#include "common.cuh"
+
+namespace lr {
+namespace glu {
+
+// s = sigmoid(a), i = 1 - s, both to a few ulp (e held below 2^120 so that
+// e s stays 1 for very negative a; NaN goes through)
+__device__ __forceinline__ void sigmoid_pair(float a, float& s, float& i) {
+  float e = __expf(-a);
+  asm("min.NaN.f32 %0, %0, 0f7B800000;" : "+f"(e));
+  s = __fdividef(1.0f, 1.0f + e);
+  i = e * s;
+}
+
+constexpr float kGelu0 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGelu1 = 0.044715f;
+
+// act(g): 0 silu g s(g); 1 gelu, tanh form: (1 + tanh a) / 2 = s(2a), so
+// g s(2a); 2 sigmoid
+__device__ __forceinline__ float value(float g, int act) {
+  float s, i;
+  sigmoid_pair(act == 1 ? kGelu0 * g * fmaf(kGelu1 * g, g, 1.f) : g, s, i);
+  return act == 2 ? s : g * s;
+}
+// act(g) and act'(g)
+__device__ __forceinline__ void value_slope(float g, int act, float& v, float& d) {
+  float s, i;
+  sigmoid_pair(act == 1 ? kGelu0 * g * fmaf(kGelu1 * g, g, 1.f) : g, s, i);
+  const float si = s * i;
+  const float da = act == 1 ? kGelu0 * fmaf(3.f * kGelu1 * g, g, 1.f) : 1.f;
+  v = act == 2 ? s : g * s;
+  d = act == 2 ? si : fmaf(g * da, si, s);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a warp's staged box (32 rows of 64 bf16, 16-byte piece j of row r at piece
+// j ^ (r & 7)) to rows row0.., columns col0.. by plain stores
+__device__ __forceinline__ void store_rows(uint32_t box, bf16* out, int64_t ld, int row0, int col0,
+                                           int rows, int cols, int lane) {
+  for (int r = 0; r < 32 && row0 + r < rows; ++r) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];"
+                 : "=r"(v)
+                 : "r"(box + (uint32_t)(r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4)));
+    unsigned short* o =
+        reinterpret_cast<unsigned short*>(out) + (int64_t)(row0 + r) * ld + col0 + 2 * lane;
+    if (col0 + 2 * lane < cols) o[0] = (unsigned short)v;
+    if (col0 + 2 * lane + 1 < cols) o[1] = (unsigned short)(v >> 16);
+  }
+}
+
+}  // namespace glu
+}  // namespace lr

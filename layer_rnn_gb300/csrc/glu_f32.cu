@@ -1,0 +1,461 @@
+// Gated feed-forward, float32, on the tensor cores.  The products and their
+// order are those of the bfloat16 kernel (glu.cu): forward, dgu (the same
+// product again with the gradients of the pre-activations as epilogue), dx, dW.
+//
+// Operands are scaled fp16 pairs, x s = hi + lo (s a power of two that maps the
+// operand's largest magnitude below 2^14): hi hi + hi lo + lo hi, about 22 bits
+// of every value near the largest.
+//
+// The sums need more than that.  The tensor core cuts off what does not fit
+// when it adds to its float32 accumulator; over a contraction of 1000 that
+// pulled results towards zero by 1.3e-5, ten times a float32 product's error.
+// So hi hi goes to an accumulator that holds 64 k at a time, four MMAs; the
+// epilogue warps add it to sums in registers, rounding to nearest, while the
+// MMAs fill another.  The small products, 2^-11 of it, keep one accumulator
+// each tile.  Tensor memory: two accumulators of 128 columns for hi hi, two for
+// the rest (this tile's and the next one's).
+//
+// A pair of blocks works on 256 x 128 of a result (forward and dgu: 64
+// features).  Bound by the tensor cores at three passes a product; adding up
+// takes a third of that time beside them.  Every wait is bounded.
+#include <cuda_fp16.h>
+
+#include "gemm.h"
+#include "glu_tc.cuh"
+
+namespace lr {
+namespace {
+
+using namespace glu;
+
+constexpr int kCols = 128;             // columns of a pair's tile
+constexpr int kA = kHalf * 128;        // bytes: a block's rows, 64 k, hi or lo
+constexpr int kB = 64 * 128;           // a block's half of the columns
+constexpr int kStage = 2 * (kA + kB);
+constexpr int ST = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kSmem = ST * kStage + 1024;
+
+struct Maps {
+  CUtensorMap ah, al, bh, bl;
+};
+
+// the scale that maps the largest magnitude (bit pattern mb) into
+// [2^13, 2^14) is 2^this; the pairs are made with the same rule
+__device__ __forceinline__ float unscale(unsigned mb) {
+  if (mb == 0 || mb >= 0x7f800000u) return 1.f;
+  const int s = min(max(13 - ((int)(mb >> 23) - 127), -126), 126);
+  return __int_as_float((127 - s) << 23);
+}
+
+template <int PROD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    glu_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  constexpr bool kAmn = PROD == kDw, kBmn = PROD == kDx || PROD == kDw;
+  constexpr bool kGated = PROD == kForward || PROD == kDgu;
+  // kind::f16, fp16 operands, float32 sums, M = 256, N = 128
+  constexpr uint32_t kIdesc = (1u << 4) | ((kAmn ? 1u : 0u) << 15) | ((kBmn ? 1u : 0u) << 16) |
+                              ((uint32_t)(kCols >> 3) << 17) | ((uint32_t)(2 * kHalf >> 4) << 24);
+  __shared__ __align__(8) uint64_t bars[2 * ST + 4];
+  __shared__ uint32_t tmem_slot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned rank = tc::cl_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t full0 = tc::smem_addr(&bars[0]), empty0 = full0 + 8 * ST;
+  const uint32_t tfull0 = empty0 + 8 * ST, tempty0 = tfull0 + 16;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      tc::mbar_init(full0 + 8 * s, 1);
+      tc::mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tfull0 + 8 * i, 1);
+      tc::mbar_init(tempty0 + 8 * i, 2 * kEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     tc::smem_addr(&tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::cl_sync();
+  tc::fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  Walk w;
+  walk_start(p, w, pair, pairs);
+  if (threadIdx.x == 0) {
+    // loads, in both blocks
+    int s = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    while (ok && walk_next(p, w, pairs)) {
+      int z, mt, nt;
+      tile_at(p, w.tile, z, mt, nt);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (!tc::mbar_wait_cluster_bounded(empty0 + 8 * s, ph, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        const uint32_t a = base + (uint32_t)(s * kStage), b = a + 2 * kA;
+        if (rank == 0) tc::mbar_arrive_expect_tx(full0 + 8 * s, 2 * kStage);
+        const uint32_t bar = map_rank(full0 + 8 * s, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const CUtensorMap* ma = h ? &maps.al : &maps.ah;
+          const CUtensorMap* mb = h ? &maps.bl : &maps.bh;
+          const uint32_t at = a + h * kA, bt = b + h * kB;
+          if (kGated) {
+            load_box(at, ma, kb * 64, mt * 2 * kHalf + (int)rank * kHalf, 0, bar);
+            load_box(bt, mb, kb * 64, nt * 64, (int)rank, bar);
+          } else if (PROD == kDx) {
+            const int pl = kb >= p.kb_plane, k = (kb - pl * p.kb_plane) * 64;
+            load_box(at, ma, k, mt * 2 * kHalf + (int)rank * kHalf, pl, bar);
+            load_box(bt, mb, nt * kCols + (int)rank * 64, k, pl, bar);
+          } else {
+            const int f0 = mt * 2 * kHalf + (int)rank * kHalf;
+            load_box(at, ma, f0, kb * 64, z, bar);
+            load_box(at + 8192, ma, f0 + 64, kb * 64, z, bar);
+            load_box(bt, mb, nt * kCols + (int)rank * 64, kb * 64, 0, bar);
+          }
+        }
+        if (++s == ST) { s = 0; ph ^= 1u; }
+      }
+    }
+    if (!ok) {
+      // copies in flight land within microseconds: stay that long
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else if (threadIdx.x == 32 && rank == 0) {
+    // MMAs, for both blocks
+    int s = 0, blk = 0, n = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    while (ok && walk_next(p, w, pairs)) {
+      const uint32_t d1 = tmem + 256u + (uint32_t)((n & 1) * kCols);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
+        const int buf = blk & 1;
+        if (!tc::mbar_wait_cluster_bounded(tempty0 + 8 * buf, ((blk >> 1) & 1) ^ 1u, p.status,
+                                           p.timeout_ns) ||
+            !tc::mbar_wait_cluster_bounded(full0 + 8 * s, ph, p.status, p.timeout_ns)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        const uint32_t a = base + (uint32_t)(s * kStage), b = a + 2 * kA;
+        const uint64_t ah = operand_desc<kAmn>(a), al = operand_desc<kAmn>(a + kA);
+        const uint64_t bh = operand_desc<kBmn>(b), bl = operand_desc<kBmn>(b + kB);
+        const uint32_t d0 = tmem + (uint32_t)(buf * kCols);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t sa = (uint64_t)(kk * (kAmn ? 128 : 2)), sb = (uint64_t)(kk * (kBmn ? 128 : 2));
+          mma2(d0, ah + sa, bh + sb, kIdesc, kk > 0 ? 1u : 0u);
+          mma2(d1, ah + sa, bl + sb, kIdesc, (kb > w.kb0 || kk > 0) ? 1u : 0u);
+          mma2(d1, al + sa, bh + sb, kIdesc, 1u);
+        }
+        commit2(empty0 + 8 * s);
+        commit2(tfull0 + 8 * buf);
+        if (++s == ST) { s = 0; ph ^= 1u; }
+      }
+      ++n;
+    }
+  } else if (warp >= 2) {
+    // warp e adds up rows 32 (warp % 4).. of two runs of 32 columns: where gate
+    // and up columns belong together, the same features of both
+    const int e = warp - 2, q = warp & 3, half = e >> 2;
+    const int c0 = kGated ? 32 * half : 64 * half, c1 = kGated ? 64 + 32 * half : 64 * half + 32;
+    const uint32_t tempty = map_rank(tempty0, 0);
+    const float ia = unscale(*p.amax), ib = unscale(*p.bmax);
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    const bool vec = p.tma_out != 0;  // rows of float4
+    unsigned mx = 0;
+    int blk = 0, n = 0;
+    bool ok = true;
+    while (ok && walk_next(p, w, pairs)) {
+      __syncwarp();  // rows past the end skip their stores
+      int z, mt, nt;
+      tile_at(p, w.tile, z, mt, nt);
+      float s0[32], s1[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s0[i] = s1[i] = 0.f;
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
+        const int buf = blk & 1;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_cluster_bounded(
+                                         tfull0 + 8 * buf, (blk >> 1) & 1, p.status, p.timeout_ns))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        float v[32];
+        tc::tmem_ld32(lanes + (uint32_t)(buf * kCols + c0), v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s0[i] += v[i];
+        tc::tmem_ld32(lanes + (uint32_t)(buf * kCols + c1), v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s1[i] += v[i];
+        if (kb == w.kb1 - 1) {  // the small products, before the next tile's may begin
+          const uint32_t d1 = lanes + 256u + (uint32_t)((n & 1) * kCols);
+          tc::tmem_ld32(d1 + (uint32_t)c0, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s0[i] = (s0[i] + v[i]) * ia * ib;
+          tc::tmem_ld32(d1 + (uint32_t)c1, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s1[i] = (s1[i] + v[i]) * ia * ib;
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at(tempty + 8 * buf);
+      }
+      if (!ok) break;
+      ++n;
+      if (w.partial) {
+        float4* d = part_at<kCols>(p, pair, w.slot, (int)rank * 4 + q) + lane;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          __stcs(d + (c0 / 4 + i) * 32, make_float4(s0[4 * i], s0[4 * i + 1], s0[4 * i + 2], s0[4 * i + 3]));
+          __stcs(d + (c1 / 4 + i) * 32, make_float4(s1[4 * i], s1[4 * i + 1], s1[4 * i + 2], s1[4 * i + 3]));
+        }
+        continue;
+      }
+      const int row = mt * 2 * kHalf + (int)rank * kHalf + q * 32 + lane;
+      if (row >= p.rows) continue;
+      if (kGated) {
+        const int f0 = nt * 64 + half * 32;
+        if (PROD == kForward) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s0[i] = value(s0[i], p.act) * s1[i];
+        } else {
+          const float* dy = static_cast<const float*>(p.dy) + (int64_t)row * p.ld_dy + f0;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float v, d;
+            value_slope(s0[i], p.act, v, d);
+            const float y = f0 + i < p.cols ? __ldg(dy + i) : 0.f;
+            s0[i] = y * s1[i] * d;
+            s1[i] = y * v;
+            mx = max(mx, max(__float_as_uint(s0[i]) & 0x7fffffffu, __float_as_uint(s1[i]) & 0x7fffffffu));
+          }
+        }
+#pragma unroll
+        for (int pl = 0; pl < (PROD == kDgu ? 2 : 1); ++pl) {
+          float* o = static_cast<float*>(p.out) + ((int64_t)pl * p.rows + row) * p.ld_out + f0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float v[4] = {pl ? s1[4 * i] : s0[4 * i], pl ? s1[4 * i + 1] : s0[4 * i + 1],
+                                pl ? s1[4 * i + 2] : s0[4 * i + 2], pl ? s1[4 * i + 3] : s0[4 * i + 3]};
+            if (vec && f0 + 4 * i < p.cols) store4(o + 4 * i, v);
+            if (!vec)
+              for (int u = 0; u < 4; ++u)
+                if (f0 + 4 * i + u < p.cols) o[4 * i + u] = v[u];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = nt * kCols + (h ? c1 : c0);
+          float* o = static_cast<float*>(p.out) + ((int64_t)z * p.rows + row) * p.ld_out + col;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float v[4] = {h ? s1[4 * i] : s0[4 * i], h ? s1[4 * i + 1] : s0[4 * i + 1],
+                                h ? s1[4 * i + 2] : s0[4 * i + 2], h ? s1[4 * i + 3] : s0[4 * i + 3]};
+            if (vec && col + 4 * i < p.cols) store4(o + 4 * i, v);
+            if (!vec)
+              for (int u = 0; u < 4; ++u)
+                if (col + 4 * i + u < p.cols) o[4 * i + u] = v[u];
+          }
+        }
+      }
+    }
+    if (PROD == kDgu) {
+      __syncwarp();
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0) atomicMax(p.omax, mx);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::cl_sync();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+template <int PROD>
+cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+  auto kernel = glu_f32_kernel<PROD>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = plan_pairs(&p, a.num_sms, 16);  // 128 KB each way
+  p.group = std::min(p.m_tiles, 16);
+  p.tma_out = p.ld_out % 4 == 0 && p.cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
+  p.status = a.status;
+  p.timeout_ns = 2000000000LL;
+  kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  e = cudaGetLastError();
+  const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
+  if (e != cudaSuccess || cut_tiles == 0) return e;
+  glu_join_kernel<float, kCols><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError();
+}
+
+struct Pairs {
+  char* hi = nullptr;
+  char* lo = nullptr;
+  int64_t ld = 0;
+};
+int64_t pair_bytes(int64_t rows, int64_t cols) { return 2 * round256(rows * pad8(cols) * 2); }
+
+struct Room {
+  char* at;
+  char* take(int64_t bytes) {
+    char* p = at;
+    at += round256(bytes);
+    return p;
+  }
+  Pairs pairs(int64_t rows, int64_t cols) {
+    Pairs q;
+    q.ld = pad8(cols);
+    q.hi = take(rows * q.ld * 2);
+    q.lo = take(rows * q.ld * 2);
+    return q;
+  }
+};
+
+#define TRY(call)                  \
+  do {                             \
+    const cudaError_t e_ = (call); \
+    if (e_ != cudaSuccess) return e_; \
+  } while (0)
+
+// src [rows][cols], row pitch lds, to pairs, with the scale of *mx
+cudaError_t split(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& q,
+                  const unsigned* mx, cudaStream_t st) {
+  return split_f16_operand(src, rows, cols, lds, q.hi, q.lo, q.ld, false, mx, st);
+}
+
+// x and W as pairs; mx[0], mx[1] their largest magnitudes
+cudaError_t operands(const GluArgs& a, unsigned* mx, const Pairs& x, const Pairs& w,
+                     cudaStream_t st) {
+  const float* xf = static_cast<const float*>(a.x);
+  const float* wf = static_cast<const float*>(a.W);
+  TRY(cudaMemsetAsync(mx, 0, 256, st));
+  TRY(absmax_operand(xf, a.M, a.K, a.K, mx, a.num_sms, st));
+  TRY(absmax_operand(wf, 2 * a.F, a.K, a.K, mx + 1, a.num_sms, st));
+  TRY(split(xf, a.M, a.K, a.K, x, mx, st));
+  return split(wf, 2 * a.F, a.K, a.K, w, mx + 1, st);
+}
+
+bool gated_maps(const GluArgs& a, const Pairs& x, const Pairs& w, Maps* m) {
+  return map3(&m->ah, x.hi, a.K, a.M, 1, x.ld, a.M, 128) &&
+         map3(&m->al, x.lo, a.K, a.M, 1, x.ld, a.M, 128) &&
+         map3(&m->bh, w.hi, a.K, a.F, 2, w.ld, a.F, 64) &&
+         map3(&m->bl, w.lo, a.K, a.F, 2, w.ld, a.F, 64);
+}
+
+P gated(const GluArgs& a, const unsigned* mx) {
+  P p = {};
+  p.m_tiles = (int)ceil_div(a.M, 2 * kHalf);
+  p.n_tiles = (int)ceil_div(a.F, 64);
+  p.planes = 1;
+  p.nkb = (int)ceil_div(a.K, 64);
+  p.rows = (int)a.M; p.cols = (int)a.F;
+  p.act = a.act;
+  p.amax = mx; p.bmax = mx + 1;
+  return p;
+}
+
+}  // namespace
+
+int64_t glu_f32_workspace(int64_t M, int64_t K, int64_t F, bool backward) {
+  const int64_t fwd = 256 + pair_bytes(M, K) + pair_bytes(2 * F, K);
+  if (!backward) return fwd;
+  return fwd + round256(2 * M * pad8(F) * 4) + pair_bytes(2 * M, F) +
+         (int64_t)kGluMaxPairs * 2 * 2 * kHalf * kCols * 4;
+}
+
+cudaError_t glu_f32_forward(const GluArgs& a, cudaStream_t st) {
+  Room room{static_cast<char*>(a.workspace)};
+  unsigned* mx = reinterpret_cast<unsigned*>(room.take(256));
+  const Pairs x = room.pairs(a.M, a.K), w = room.pairs(2 * a.F, a.K);
+  TRY(operands(a, mx, x, w, st));
+  Maps maps = {};
+  if (!gated_maps(a, x, w, &maps)) return cudaErrorInvalidValue;
+  P p = gated(a, mx);
+  p.out = a.y; p.ld_out = a.F;
+  return launch<kForward>(maps, p, a, st);
+}
+
+cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
+  Room room{static_cast<char*>(a.workspace)};
+  unsigned* mx = reinterpret_cast<unsigned*>(room.take(256));
+  const Pairs x = room.pairs(a.M, a.K), w = room.pairs(2 * a.F, a.K);
+  const int64_t Fp = pad8(a.F);
+  float* dgu = reinterpret_cast<float*>(room.take(2 * a.M * Fp * 4));
+  const Pairs d = room.pairs(2 * a.M, a.F);
+  float* part = reinterpret_cast<float*>(room.at);
+  TRY(operands(a, mx, x, w, st));
+  {
+    Maps maps = {};
+    if (!gated_maps(a, x, w, &maps)) return cudaErrorInvalidValue;
+    P p = gated(a, mx);
+    p.dy = a.dy; p.ld_dy = a.F;
+    p.out = dgu; p.ld_out = Fp;
+    p.omax = mx + 2;
+    TRY(launch<kDgu>(maps, p, a, st));
+  }
+  TRY(split(dgu, 2 * a.M, a.F, Fp, d, mx + 2, st));
+  P p = {};
+  p.n_tiles = (int)ceil_div(a.K, kCols);
+  p.cols = (int)a.K;
+  p.ld_out = a.K;
+  p.amax = mx + 2;
+  p.part = part;
+  if (a.dx) {
+    Maps m = {};
+    if (!map3(&m.ah, d.hi, a.F, a.M, 2, Fp, a.M, 128) ||
+        !map3(&m.al, d.lo, a.F, a.M, 2, Fp, a.M, 128) ||
+        !map3(&m.bh, w.hi, a.K, a.F, 2, w.ld, a.F, 64) ||
+        !map3(&m.bl, w.lo, a.K, a.F, 2, w.ld, a.F, 64))
+      return cudaErrorInvalidValue;
+    p.m_tiles = (int)ceil_div(a.M, 2 * kHalf);
+    p.planes = 1;
+    p.kb_plane = (int)ceil_div(a.F, 64);
+    p.nkb = 2 * p.kb_plane;
+    p.rows = (int)a.M;
+    p.out = a.dx;
+    p.bmax = mx + 1;
+    TRY(launch<kDx>(m, p, a, st));
+  }
+  if (a.dW) {
+    Maps m = {};
+    if (!map3(&m.ah, d.hi, a.F, a.M, 2, Fp, a.M, 64) ||
+        !map3(&m.al, d.lo, a.F, a.M, 2, Fp, a.M, 64) ||
+        !map3(&m.bh, x.hi, a.K, a.M, 1, x.ld, a.M, 64) ||
+        !map3(&m.bl, x.lo, a.K, a.M, 1, x.ld, a.M, 64))
+      return cudaErrorInvalidValue;
+    p.m_tiles = (int)ceil_div(a.F, 2 * kHalf);
+    p.planes = 2;
+    p.kb_plane = 0;
+    p.nkb = (int)ceil_div(a.M, 64);
+    p.rows = (int)a.F;
+    p.out = a.dW;
+    p.bmax = mx;
+    TRY(launch<kDw>(m, p, a, st));
+  }
+  return cudaSuccess;
+}
+
+}  // namespace lr

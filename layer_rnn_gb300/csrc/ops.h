@@ -47,4 +47,34 @@ struct W4Args {
 cudaError_t w4_matvec(const W4Args& a, cudaStream_t st);
 cudaError_t w4_quantize(const W4Args& a, const void* w, cudaStream_t st);
 
+// ---------------------------------------------------------------------------
+// gated feed-forward
+// ---------------------------------------------------------------------------
+constexpr int kGluMaxPairs = 80;  // pairs of blocks of the tensor-core kernel at most
+
+struct GluArgs {
+  int64_t M = 0, K = 0, F = 0;
+  int act = 0, bf16 = 0;
+  const void* x = nullptr;    // [M, K]
+  const void* W = nullptr;    // [2F, K]: gate rows, then up rows
+  void* y = nullptr;          // [M, F]
+  const void* dy = nullptr;   // backward
+  void* dx = nullptr;         // or null
+  void* dW = nullptr;         // or null
+  void* workspace = nullptr;
+  int num_sms = 0;
+  int* status = nullptr;
+};
+// bfloat16, many rows (glu.cu)
+int64_t glu_tc_workspace(int64_t M, int64_t K, int64_t F, bool backward);
+cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st);
+cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st);
+
+// few rows, either type; the workspace is not used (glu_rows.cu)
+cudaError_t glu_rows_forward(const GluArgs& a, cudaStream_t st);
+// float32, many rows (glu_f32.cu)
+int64_t glu_f32_workspace(int64_t M, int64_t K, int64_t F, bool backward);
+cudaError_t glu_f32_forward(const GluArgs& a, cudaStream_t st);
+cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st);
+
 }  // namespace lr

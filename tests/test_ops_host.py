@@ -98,3 +98,31 @@ def test_w4_refuses(L, h):
     quant = lambda R=4, K=64, group=32, W=P, q=P, ldq=0, s=P, z=None: L.rnn_w4_quantize(  # noqa: E731
         h, None, R, K, group, W, q, ldq, s, z)
     assert quant(W=None) == INVALID and quant(group=8) == INVALID and quant(W=ODD) == MISALIGNED
+
+
+def test_glu_workspace_and_refusals(L, h):
+    b = ctypes.c_int64()
+    size = lambda M, K, F, bwd: (L.rnn_glu_workspace_size(h, M, K, F, bwd, ctypes.byref(b)), b.value)  # noqa: E731
+    assert size(1, 64, 64, 0) == (OK, 256)
+    assert size(1000, 64, 64, 1)[1] >= size(1000, 64, 64, 0)[1] >= 256
+    assert size(1000, 64, 64, 1)[1] >= 2 * 1000 * 64 * 2
+    for bad in ((0, 1, 1, 0), (1, 0, 1, 0), (1, 1, 0, 0), (1, 1, 1, 2)):
+        assert size(*bad)[0] == INVALID
+    assert size(1 << 24, 1, 1, 0)[0] == UNSUPPORTED and size(1, 1, 1 << 23, 0)[0] == UNSUPPORTED
+
+    def fwd(M=4, K=8, F=8, act=0, x=P, W=P, y=P, ws=P, nb=1 << 40):
+        return L.rnn_glu_forward(h, None, M, K, F, act, x, W, y, ws, nb)
+
+    def bwd(M=4, K=8, F=8, act=0, x=P, W=P, dy=P, dx=P, dW=P, ws=P, nb=1 << 40):
+        return L.rnn_glu_backward(h, None, M, K, F, act, x, W, dy, dx, dW, ws, nb)
+
+    for call in (fwd, bwd):
+        for bad in (dict(M=0), dict(K=-1), dict(F=0), dict(act=3), dict(act=-1), dict(x=None), dict(W=None),
+                    dict(ws=None)):
+            assert call(**bad) == INVALID, bad
+        for bad in (dict(x=ODD), dict(W=ODD), dict(ws=P + 16)):
+            assert call(**bad) == MISALIGNED, bad
+        assert call(M=1 << 25) == UNSUPPORTED
+        assert call(M=300, nb=255) == SMALL
+    assert fwd(y=None) == INVALID and fwd(y=ODD) == MISALIGNED
+    assert bwd(dy=None) == INVALID and bwd(dx=None, dW=None) == INVALID and bwd(dW=ODD) == MISALIGNED
