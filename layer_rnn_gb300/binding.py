@@ -392,6 +392,7 @@ class Ops:
         self.torch = torch
         self.dtype = dtype
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.h = None
         h = _vp()
         _call("rnn_ops_create", ctypes.byref(h), DTYPES[dtype], flags)
@@ -409,8 +410,13 @@ class Ops:
             pass
 
     def _stream(self, stream):
-        s = stream if stream is not None else self.torch.cuda.current_stream()
-        return s.cuda_stream
+        if stream is not None:
+            return stream.cuda_stream
+        # the address of the current stream without a Stream object around it:
+        # 3 us less in a call of 10
+        if self._raw_stream is not None:
+            return self._raw_stream(self.torch.cuda.current_device())
+        return self.torch.cuda.current_stream().cuda_stream
 
     def _check(self, name, t, shape, dtype=None):
         """A dense tensor of this shape (or None): its address."""

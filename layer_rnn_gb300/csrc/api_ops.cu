@@ -93,6 +93,7 @@ ScanArgs scan_args(const rnn_ops* h, int64_t T, int64_t N, int64_t H, int D, int
   a.lengths = lengths;
   a.gx = gx; a.ldg = ldg; a.ldy = ldy;
   a.num_sms = h->num_sms;
+  a.status = h->d_status;
   return a;
 }
 

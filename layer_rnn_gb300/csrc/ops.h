@@ -27,6 +27,7 @@ struct ScanArgs {
   void* dgx = nullptr;                // row pitch ldg
   float* dh0 = nullptr;
   int num_sms = 0;
+  int* status = nullptr;
 };
 cudaError_t scan_forward(const ScanArgs& a, cudaStream_t st);
 cudaError_t scan_backward(const ScanArgs& a, cudaStream_t st);

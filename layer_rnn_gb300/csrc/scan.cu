@@ -17,10 +17,14 @@
 // kScanState steps and the backward composes the rest of the tile again.
 //
 // Bound by memory: 10 to 20 flop for every 4 to 16 bytes.
+#include <cuda.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "ops.h"
+#include "tc_common.cuh"
 
 namespace lr {
 namespace {
@@ -29,13 +33,26 @@ constexpr int kThreads = 256;
 
 // f = sigmoid(p) and i = 1 - f, both to a few ulp: e = e^-p, f = 1 / (1 + e),
 // i = e f.  e is held below 2^120 so that e f stays 1 where p is very
-// negative; NaN goes through.
+// negative; NaN goes through.  The instructions are the ones that flush
+// denormals (an i below 2^-126 becomes 0): the others cost eight more a gate,
+// a third of the forward pass's instructions.
+__device__ __forceinline__ float exp_neg(float p) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p * -1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float recip(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ void gate_pair(float p, float& f, float& i) {
-  float e = __expf(-p);
+  float e = exp_neg(p);
   asm("min.NaN.f32 %0, %0, 0f7B800000;" : "+f"(e));
-  f = __fdividef(1.0f, 1.0f + e);
+  f = recip(1.0f + e);
   i = e * f;
 }
+__device__ __forceinline__ float gate_one(float p) { return recip(1.0f + exp_neg(p)); }
 
 // V consecutive elements of storage type E, held raw
 template <typename E, int V> struct Raw;
@@ -451,6 +468,597 @@ __global__ void __launch_bounds__(kThreads) scan_backward_kernel(const ScanP p) 
     p.dh0[kc.state + c % V] = carry;
 }
 
+// ---------------------------------------------------------------------------
+// Rows that TMA can read: a block takes 128 bytes of a row (64 bf16 or 32
+// float32 channels of one sequence and direction), each of its four warps 16
+// consecutive steps, a lane a 4-byte word.  Tiles of 64 steps arrive in a ring
+// of shared memory, so that the loads of the next tiles run under the
+// arithmetic of this one; every input is still read once from memory.
+//
+// The arithmetic comes close to the memory's time (25 instructions an element
+// forward, 50 backward), hence four warps with 16 steps each rather than eight
+// with 8: joining slots costs half as much an element.  Blocks of a cluster
+// exchange their tiles' maps by asynchronous stores that count on a barrier of
+// the receiver; a cluster-wide barrier instead cost 5 us a round.
+// ---------------------------------------------------------------------------
+constexpr int kWarps = 4, kSteps = 16, kTileSteps = kWarps * kSteps;
+constexpr int kRow = 128, kPlane = kTileSteps * kRow;
+static_assert(kTileSteps == kScanState, "a tile starts at a saved state");
+
+struct TileP {
+  CUtensorMap gx, dy;
+  int T, N, H, D, groups_h;  // groups_h: channel groups of a direction
+  int64_t ldg, ldy;
+  const int* lengths;
+  const float* h0;
+  void* y;
+  float* hy;
+  float* states;
+  const float* dhy;
+  void* dgx;
+  float* dh0;
+  int* status;
+};
+
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, int x, int n, int t,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(n), "r"(t), "r"(bar)
+      : "memory");
+}
+
+// V channels of a lane from its word
+template <typename E> struct Word;
+template <> struct Word<bf16> {
+  static constexpr int V = 2;
+  static __device__ __forceinline__ void get(uint32_t w, float (&v)[2]) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t put(const float (&v)[2]) { return pack2(v[0], v[1]); }
+};
+template <> struct Word<float> {
+  static constexpr int V = 1;
+  static __device__ __forceinline__ void get(uint32_t w, float (&v)[1]) { v[0] = __uint_as_float(w); }
+  static __device__ __forceinline__ uint32_t put(const float (&v)[1]) { return __float_as_uint(v[0]); }
+};
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// maps of V channels, one lane: (A, B) pairs
+template <int V> struct alignas(8 * V) MapV { float2 m[V]; };
+
+// this block's map to block `rank`, counting on the barrier at `bar` there
+template <int V>
+__device__ __forceinline__ void push(uint32_t local, uint32_t bar, unsigned rank,
+                                     const float (&A)[V], const float (&B)[V]) {
+  uint32_t at, rbar;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rbar) : "r"(bar), "r"(rank));
+  if (V == 2)
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+            at),
+        "f"(A[0]), "f"(B[0]), "f"(A[V - 1]), "f"(B[V - 1]), "r"(rbar)
+        : "memory");
+  else
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+        "f"(A[0]), "f"(B[0]), "r"(rbar)
+        : "memory");
+}
+
+typedef std::integral_constant<bool, true> Yes;
+typedef std::integral_constant<bool, false> No;
+constexpr long long kWaitNs = 2000000000LL;
+
+// Where a block works, and which steps of its sequence count, in walk order
+// [va, vb).
+template <typename E>
+struct Place {
+  static constexpr int V = Word<E>::V, kCh = 32 * V;
+  int n, d, j0, j, va, vb;
+  bool live;
+  int64_t state, gh;
+  __device__ __forceinline__ Place(const TileP& p, int group) {
+    const int lane = threadIdx.x & 31;
+    const int nd = group / p.groups_h;
+    n = nd / p.D;
+    d = nd - n * p.D;
+    j0 = (group - nd * p.groups_h) * kCh;
+    j = j0 + lane * V;
+    live = j < p.H;
+    state = ((int64_t)d * p.N + n) * p.H + j;
+    gh = (int64_t)nd * p.H + j;
+    const int len = p.lengths ? min(max(p.lengths[n], 0), p.T) : p.T;
+    va = d ? p.T - len : 0;
+    vb = d ? p.T : len;
+  }
+};
+
+// One tile's words of a lane: 16-byte piece c of row r lies at piece
+// c ^ (r & 7).  Step k of a warp is row 16 warp + k, or, walking backwards, row
+// 63 - (16 warp + k); both have k's low bits, straight or inverted.
+struct Words {
+  uint32_t at[8];  // step k & 7, without the warp's rows
+  int32_t eight;   // bytes from step k to step k + 8
+  __device__ __forceinline__ Words(int warp, int d) {
+    const int lane = threadIdx.x & 31, piece = (lane >> 2) ^ (d ? 7 : 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = d ? kTileSteps - 1 - (warp * kSteps + k) : warp * kSteps + k;
+      at[k] = (uint32_t)(row * kRow + ((piece ^ k) << 4) + (lane & 3) * 4);
+    }
+    eight = d ? -8 * kRow : 8 * kRow;
+  }
+  __device__ __forceinline__ uint32_t get(uint32_t plane, int k) const {
+    return lds32(plane + at[k & 7] + (k >= 8 ? eight : 0));
+  }
+};
+
+// The maps of a tile's warps, joined; the state (or gradient) into each warp's
+// steps and past the whole round.  ORDER: the warps in the walk's order (+1) or
+// against it (-1).
+template <int V, int ORDER>
+struct Chain {
+  float pA[V], pB[V], A[V], B[V];
+  __device__ __forceinline__ void join(const MapV<V> (&map)[kWarps][32], int warp, int lane) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) { A[v] = pA[v] = 1.f; B[v] = pB[v] = 0.f; }
+#pragma unroll
+    for (int w0 = 0; w0 < kWarps; ++w0) {
+      const int w = ORDER > 0 ? w0 : kWarps - 1 - w0;
+      const MapV<V> m = map[w][lane];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (w == warp) { pA[v] = A[v]; pB[v] = B[v]; }
+        B[v] = fmaf(m.m[v].x, B[v], m.m[v].y);
+        A[v] *= m.m[v].x;
+      }
+    }
+  }
+  // to every block of the cluster
+  __device__ __forceinline__ void send(MapV<V>* tile_map, uint32_t bar, unsigned rank,
+                                       unsigned csize, int warp, int lane) {
+    const uint32_t at = tc::smem_addr(tile_map + rank * 32 + lane);
+    if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(bar, csize * 32 * sizeof(MapV<V>));
+    for (unsigned c = warp; c < csize; c += kWarps) push<V>(at, bar, c, A, B);
+  }
+  // `in`: the value into this warp's steps; `carry` moves past the round
+  __device__ __forceinline__ void receive(const MapV<V>* tile_map, uint32_t bar, uint32_t parity,
+                                          unsigned rank, unsigned csize, int lane, int* status,
+                                          float (&carry)[V], float (&in)[V]) {
+    if (csize > 1) {
+      tc::mbar_wait_cluster_bounded(bar, parity, status, kWaitNs);
+      __syncwarp();
+      for (unsigned c = 0; c < csize; ++c) {
+        const MapV<V> m = tile_map[c * 32 + lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (c == rank) in[v] = carry[v];
+          carry[v] = fmaf(m.m[v].x, carry[v], m.m[v].y);
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) in[v] = fmaf(pA[v], in[v], pB[v]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        in[v] = fmaf(pA[v], carry[v], pB[v]);
+        carry[v] = fmaf(A[v], carry[v], B[v]);
+      }
+    }
+  }
+};
+
+// The ring of tiles: `planes` planes of 64 rows of 128 bytes a stage
+struct Ring {
+  uint32_t base, bar0, phase = 0;
+  __device__ __forceinline__ Ring(unsigned char* smem, uint64_t* bars, int n) {
+    base = (tc::smem_addr(smem) + 1023u) & ~1023u;
+    bar0 = tc::smem_addr(bars);
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < n; ++s) tc::mbar_init(bar0 + 8 * s, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (cluster_size() > 1) cluster_sync();  // every block runs before it is written to
+  }
+  __device__ __forceinline__ void wait(int s, int* status) {
+    tc::mbar_wait_bounded(bar0 + 8 * s, (phase >> s) & 1u, status, kWaitNs);
+    phase ^= 1u << s;
+  }
+};
+
+template <typename E, bool GATE, int ST>
+__global__ void __launch_bounds__(32 * kWarps, 3)
+    scan_forward_tiles(const __grid_constant__ TileP p) {
+  constexpr int G = GATE ? 3 : 2, V = Word<E>::V, L = kSteps;
+  constexpr int kStage = G * kPlane;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[ST + 2];
+  __shared__ __align__(16) MapV<V> map[2][kWarps][32];
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const unsigned csize = cluster_size(), rank = cluster_rank();
+  const Place<E> at(p, (int)(blockIdx.x / csize));
+  Ring ring(smem_raw, bars, ST + 2);
+  // the cluster's tiles: [parity of the round][block][lane]
+  MapV<V>* tile_map = reinterpret_cast<MapV<V>*>(smem_raw + (ring.base - tc::smem_addr(smem_raw)) + ST * kStage);
+  const int rounds = (int)((p.T + (int64_t)kTileSteps * csize - 1) / ((int64_t)kTileSteps * csize));
+  auto first_of = [&](int r) { return ((int64_t)r * csize + rank) * kTileSteps; };
+  auto active = [&](int64_t w0) { return w0 < at.vb && w0 + kTileSteps > at.va; };
+  auto load = [&](int r, int s) {
+    const int64_t w0 = first_of(r);
+    if (r >= rounds || !active(w0)) return;
+    const int t0 = at.d ? (int)(p.T - w0 - kTileSteps) : (int)w0;
+    const uint32_t bar = ring.bar0 + 8 * s;
+    tc::mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+    for (int b = 0; b < G; ++b)
+      tile_load(ring.base + s * kStage + b * kPlane, &p.gx, (at.d * G + b) * p.H + at.j0, at.n, t0, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int r = 0; r < ST; ++r) load(r, r);
+  const Words words(warp, at.d);
+  float carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = at.live && p.h0 ? p.h0[at.state + v] : 0.f;
+  const int64_t ty = (int64_t)p.N * p.ldy * (int64_t)sizeof(E);
+  const int64_t step = at.d ? -ty : ty;
+  char* y0 = static_cast<char*>(p.y) +
+             ((int64_t)at.n * p.ldy + (int64_t)at.d * p.H + at.j0) * (int64_t)sizeof(E);
+  int s = 0, before = ST - 1;  // this tile's stage and the last one's
+  for (int r = 0; r < rounds; ++r) {
+    __syncwarp();
+    const int par = r & 1;
+    const int64_t w0 = first_of(r), ws = w0 + warp * L;
+    const bool on = ws < at.vb && ws + L > at.va;     // this warp has steps that count
+    const bool all = ws >= at.va && ws + L <= at.vb;  // and no others
+    if (active(w0)) ring.wait(s, p.status);
+    const uint32_t stage = ring.base + s * kStage;
+    float a[L][V], b[L][V], A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
+    if (on) {
+#pragma unroll
+      for (int k = 0; k < L; ++k) {
+        float pv[V], zv[V];
+        Word<E>::get(words.get(stage, k), pv);
+        Word<E>::get(words.get(stage + kPlane, k), zv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float i;
+          gate_pair(pv[v], a[k][v], i);
+          b[k][v] = i * zv[v];
+        }
+      }
+      if (!all) {
+#pragma unroll
+        for (int k = 0; k < L; ++k) {
+          const bool ok = ws + k >= at.va && ws + k < at.vb;
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            a[k][v] = ok ? a[k][v] : 1.f;
+            b[k][v] = ok ? b[k][v] : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < L; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          B[v] = fmaf(a[k][v], B[v], b[k][v]);
+          A[v] *= a[k][v];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) map[par][warp][lane].m[v] = make_float2(A[v], B[v]);
+    __syncthreads();
+    // the tile before this one has been used by every warp
+    if (threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
+    Chain<V, 1> chain;
+    chain.join(map[par], warp, lane);
+    MapV<V>* tm = tile_map + par * csize * 32;
+    const uint32_t xbar = ring.bar0 + 8 * (ST + par);
+    if (csize > 1) chain.send(tm, xbar, rank, csize, warp, lane);
+    float o[GATE ? L : 1][V];  // under the exchange
+    if (GATE && on) {
+#pragma unroll
+      for (int k = 0; k < L; ++k) {
+        float q[V];
+        Word<E>::get(words.get(stage + 2 * kPlane, k), q);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[GATE ? k : 0][v] = gate_one(q[v]);
+      }
+    }
+    float h[V];
+    chain.receive(tm, xbar, (uint32_t)(r >> 1) & 1u, rank, csize, lane, p.status, carry, h);
+    before = s;
+    if (++s == ST) s = 0;
+    if (ws >= p.T) continue;
+    if (p.states && warp == 0 && at.live) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        p.states[ws / kScanState * ((int64_t)p.N * p.D * p.H) + at.gh + v] = h[v];
+    }
+    char* y = y0 + (at.d ? p.T - 1 - ws : ws) * ty;
+    if (on && all) {
+#pragma unroll
+      for (int k = 0; k < L; ++k, y += step) {
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = fmaf(a[k][v], h[v], b[k][v]);
+          out[v] = GATE ? h[v] * o[GATE ? k : 0][v] : h[v];
+        }
+        if (at.live) __stcs(reinterpret_cast<uint32_t*>(y) + lane, Word<E>::put(out));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < L; ++k, y += step) {
+        const bool ok = ws + k >= at.va && ws + k < at.vb;
+        float out[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] = 0.f;
+        if (on) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            h[v] = fmaf(a[k][v], h[v], b[k][v]);
+            out[v] = GATE ? h[v] * o[GATE ? k : 0][v] : h[v];
+          }
+        }
+        if (at.live && ws + k < p.T) __stcs(reinterpret_cast<uint32_t*>(y) + lane, ok ? Word<E>::put(out) : 0u);
+      }
+    }
+  }
+  if (p.hy && rank == 0 && warp == 0 && at.live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.hy[at.state + v] = carry[v];
+  }
+  if (csize > 1) cluster_sync();  // no block leaves before the others' stores to it
+}
+
+template <typename E, bool GATE, int ST>
+__global__ void __launch_bounds__(32 * kWarps, 3)
+    scan_backward_tiles(const __grid_constant__ TileP p) {
+  constexpr int G = GATE ? 3 : 2, V = Word<E>::V, L = kSteps;
+  constexpr int kStage = (G + 1) * kPlane;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[ST + 2];
+  __shared__ __align__(16) MapV<V> map[2][kWarps][32];  // against the walk
+  __shared__ float forth[2][kWarps][V][32];             // B of the walk's maps
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const unsigned csize = cluster_size(), rank = cluster_rank();
+  const Place<E> at(p, (int)(blockIdx.x / csize));
+  Ring ring(smem_raw, bars, ST + 2);
+  MapV<V>* tile_map = reinterpret_cast<MapV<V>*>(smem_raw + (ring.base - tc::smem_addr(smem_raw)) + ST * kStage);
+  const int tiles = (p.T + kTileSteps - 1) / kTileSteps;
+  const int rounds = (int)((tiles + (int64_t)csize - 1) / csize);
+  // tiles from the end of the walk; one before its start is empty
+  auto tile_of = [&](int r) { return tiles - 1 - (int64_t)r * csize - rank; };
+  auto active = [&](int64_t tile) {
+    return tile >= 0 && tile * kTileSteps < at.vb && (tile + 1) * kTileSteps > at.va;
+  };
+  auto load = [&](int r, int s) {
+    const int64_t tile = tile_of(r);
+    if (r >= rounds || !active(tile)) return;
+    const int t0 = at.d ? (int)(p.T - (tile + 1) * kTileSteps) : (int)(tile * kTileSteps);
+    const uint32_t bar = ring.bar0 + 8 * s, dst = ring.base + s * kStage;
+    tc::mbar_arrive_expect_tx(bar, kStage);
+#pragma unroll
+    for (int b = 0; b < G; ++b)
+      tile_load(dst + b * kPlane, &p.gx, (at.d * G + b) * p.H + at.j0, at.n, t0, bar);
+    tile_load(dst + G * kPlane, &p.dy, at.d * p.H + at.j0, at.n, t0, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int r = 0; r < ST; ++r) load(r, r);
+  const Words words(warp, at.d);
+  const int64_t states_row = (int64_t)p.N * p.D * p.H;
+  auto state_of = [&](int r, float (&h)[V]) {
+    const int64_t tile = tile_of(r);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      h[v] = r < rounds && active(tile) && at.live ? __ldg(p.states + tile * states_row + at.gh + v) : 0.f;
+  };
+  float carry[V], next[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = at.live && p.dhy ? p.dhy[at.state + v] : 0.f;
+  state_of(0, next);
+  const int64_t tg = (int64_t)p.N * p.ldg * (int64_t)sizeof(E);
+  const int64_t step = at.d ? tg : -tg;  // from a step to the one before it
+  const int64_t bytes_h = (int64_t)p.H * (int64_t)sizeof(E);
+  char* d0 = static_cast<char*>(p.dgx) +
+             ((int64_t)at.n * p.ldg + (int64_t)at.d * G * p.H + at.j0) * (int64_t)sizeof(E);
+  int s = 0, before = ST - 1;
+  for (int r = 0; r < rounds; ++r) {
+    __syncwarp();
+    const int par = r & 1;
+    const int64_t tile = tile_of(r), ws = tile * kTileSteps + warp * L;
+    const bool on = tile >= 0 && ws < at.vb && ws + L > at.va;
+    const bool all = on && ws >= at.va && ws + L <= at.vb;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = next[v];
+    state_of(r + 1, next);
+    if (active(tile)) ring.wait(s, p.status);
+    const uint32_t stage = ring.base + s * kStage;
+    float f[L][V], i[L][V], A[V], B[V], C[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = C[v] = 0.f; }
+    auto first_pass = [&](auto full) {
+#pragma unroll
+      for (int k = 0; k < L; ++k) {
+        float pv[V], zv[V];
+        Word<E>::get(words.get(stage, k), pv);
+        Word<E>::get(words.get(stage + kPlane, k), zv);
+        const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          gate_pair(pv[v], f[k][v], i[k][v]);
+          const float b = i[k][v] * zv[v];
+          f[k][v] = ok ? f[k][v] : 1.f;
+          A[v] *= f[k][v];
+          B[v] = fmaf(f[k][v], B[v], ok ? b : 0.f);
+        }
+      }
+#pragma unroll
+      for (int k = L - 1; k >= 0; --k) {
+        float dv[V], q[V];
+        Word<E>::get(words.get(stage + G * kPlane, k), dv);
+        if (GATE) Word<E>::get(words.get(stage + 2 * kPlane, k), q);
+        const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float direct = GATE ? dv[v] * gate_one(q[v]) : dv[v];
+          C[v] = f[k][v] * (C[v] + (ok ? direct : 0.f));
+        }
+      }
+    };
+    if (all) first_pass(Yes());
+    else if (on) first_pass(No());
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      map[par][warp][lane].m[v] = make_float2(A[v], C[v]);
+      forth[par][warp][v][lane] = B[v];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
+    Chain<V, -1> chain;
+    chain.join(map[par], warp, lane);
+    MapV<V>* tm = tile_map + par * csize * 32;
+    const uint32_t xbar = ring.bar0 + 8 * (ST + par);
+    if (csize > 1) chain.send(tm, xbar, rank, csize, warp, lane);
+    // under the exchange: the state before each step
+    float hb[L][V];
+    if (on) {
+#pragma unroll
+      for (int w = 0; w < kWarps - 1; ++w)
+        if (w < warp) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = fmaf(map[par][w][lane].m[v].x, h[v], forth[par][w][v][lane]);
+        }
+      auto states = [&](auto full) {
+#pragma unroll
+        for (int k = 0; k < L; ++k) {
+          float zv[V];
+          Word<E>::get(words.get(stage + kPlane, k), zv);
+          const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            hb[k][v] = h[v];
+            const float b = i[k][v] * zv[v];
+            h[v] = fmaf(f[k][v], h[v], ok ? b : 0.f);
+          }
+        }
+      };
+      if (all) states(Yes());
+      else states(No());
+    }
+    float c[V];
+    chain.receive(tm, xbar, (uint32_t)(r >> 1) & 1u, rank, csize, lane, p.status, carry, c);
+    before = s;
+    if (++s == ST) s = 0;
+    if (tile < 0 || ws >= p.T) continue;
+    // from the warp's last step back
+    const int64_t tl = at.d ? p.T - ws - L : ws + L - 1;
+    char* d = d0 + tl * tg;
+    if (!on) {
+      for (int k = L - 1; k >= 0; --k, d += step)
+        if (at.live && ws + k < p.T)
+          for (int b = 0; b < G; ++b) __stcs(reinterpret_cast<uint32_t*>(d + b * bytes_h) + lane, 0u);
+      continue;
+    }
+    auto gradients = [&](auto full) {
+#pragma unroll
+      for (int k = L - 1; k >= 0; --k, d += step) {
+        float zv[V], dv[V], qv[V], gp[V], gz[V], gq[V];
+        Word<E>::get(words.get(stage + kPlane, k), zv);
+        Word<E>::get(words.get(stage + G * kPlane, k), dv);
+        if (GATE) Word<E>::get(words.get(stage + 2 * kPlane, k), qv);
+        const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float o = 1.f, oi = 0.f;
+          if (GATE) gate_pair(qv[v], o, oi);
+          const float od = GATE ? o * dv[v] : dv[v];
+          const float dh = od + c[v];
+          gz[v] = dh * i[k][v];
+          gp[v] = gz[v] * (hb[k][v] - zv[v]) * f[k][v];
+          if (GATE) gq[v] = od * oi * h[v];
+          h[v] = hb[k][v];  // the state after the step before
+          c[v] = ok ? f[k][v] * dh : c[v];
+        }
+        if (at.live && (full.value || ws + k < p.T)) {
+          uint32_t* o = reinterpret_cast<uint32_t*>(d) + lane;
+          __stcs(o, ok ? Word<E>::put(gp) : 0u);
+          __stcs(reinterpret_cast<uint32_t*>(d + bytes_h) + lane, ok ? Word<E>::put(gz) : 0u);
+          if (GATE) __stcs(reinterpret_cast<uint32_t*>(d + 2 * bytes_h) + lane, ok ? Word<E>::put(gq) : 0u);
+        }
+      }
+    };
+    if (all) gradients(Yes());
+    else gradients(No());
+  }
+  if (p.dh0 && rank == 0 && warp == 0 && at.live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.dh0[at.state + v] = carry[v];
+  }
+  if (csize > 1) cluster_sync();
+}
+
+// A few steps: one thread four (or one) channels, all steps in turn.
+template <typename E, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads) scan_steps_kernel(const ScanP p) {
+  constexpr int G = GATE ? 3 : 2;
+  const Lane l = lane_of(p, (int64_t)blockIdx.x * kThreads + threadIdx.x, V, G);
+  if (!l.live) return;
+  const E* gx = static_cast<const E*>(p.gx) + l.g0;
+  E* y = static_cast<E*>(p.y) + l.y0;
+  float h[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v] = p.h0 ? p.h0[l.state + v] : 0.f;
+  if (p.states)
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.states[l.gh + v] = h[v];
+  for (int w = 0; w < (int)p.T; ++w) {
+    const int64_t t = l.d ? p.T - 1 - w : w;
+    float out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) out[v] = 0.f;
+    if (t < l.len) {
+      const E* row = gx + t * p.N * p.ldg;
+      const Raw<E, V> rp = load_raw<E, V>(row), rz = load_raw<E, V>(row + p.H);
+      Raw<E, V> rq;
+      if (GATE) rq = load_raw<E, V>(row + 2 * p.H);
+      float pv[V], zv[V], qv[V];
+      unpack(rp, pv);
+      unpack(rz, zv);
+      if (GATE) unpack(rq, qv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float f, i, o, oi;
+        gate_pair(pv[v], f, i);
+        h[v] = fmaf(f, h[v], i * zv[v]);
+        out[v] = h[v];
+        if (GATE) {
+          gate_pair(qv[v], o, oi);
+          out[v] *= o;
+        }
+      }
+    }
+    store_v(y + t * p.N * p.ldy, out);
+  }
+  if (p.hy)
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.hy[l.state + v] = h[v];
+}
+
 template <typename K>
 cudaError_t launch(K kernel, const ScanP& p, int64_t groups, int csize, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
@@ -509,15 +1117,101 @@ bool by_four(const ScanArgs& a) {
          ok(a.dgx);
 }
 
+// TMA's conditions: 16-byte rows, blocks and bases; and channels for at least
+// half a block's width
+bool by_tiles(const ScanArgs& a) {
+  const int64_t e = a.bf16 ? 2 : 4;
+  auto ok = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+  return a.H * e % 16 == 0 && a.ldg * e % 16 == 0 && a.ldy * e % 16 == 0 && ok(a.gx) && ok(a.y) &&
+         ok(a.dy) && ok(a.dgx) && a.H * e >= kRow / 2;
+}
+
+template <typename E, typename K>
+cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaStream_t st) {
+  constexpr int kCh = Word<E>::V * 32;
+  const int G = a.gate ? 3 : 2;
+  TileP p = {};
+  p.T = (int)a.T; p.N = (int)a.N; p.H = (int)a.H; p.D = (int)a.D;
+  p.groups_h = (int)((a.H + kCh - 1) / kCh);
+  p.ldg = a.ldg; p.ldy = a.ldy;
+  p.lengths = a.lengths; p.h0 = a.h0; p.y = a.y; p.hy = a.hy; p.states = a.states;
+  p.dhy = a.dhy; p.dgx = a.dgx; p.dh0 = a.dh0;
+  p.status = a.status;
+  const uint32_t box[3] = {(uint32_t)kCh, 1u, (uint32_t)kTileSteps};
+  auto map = [&](CUtensorMap* m, const void* ptr, int64_t width, int64_t ld) {
+    const uint64_t dims[3] = {(uint64_t)width, (uint64_t)a.N, (uint64_t)a.T};
+    const uint64_t strides[2] = {(uint64_t)ld * sizeof(E), (uint64_t)(a.N * ld) * sizeof(E)};
+    return tma_encode(m, 3, a.bf16, ptr, dims, strides, box);
+  };
+  if (!map(&p.gx, a.gx, a.D * G * a.H, a.ldg) || (a.dy && !map(&p.dy, a.dy, a.D * a.H, a.ldy)))
+    return cudaErrorInvalidValue;
+  // blocks of a cluster share a channel group's tiles where the groups alone
+  // give the card less than two blocks an SM
+  const int64_t groups = a.N * a.D * p.groups_h, tiles = (a.T + kTileSteps - 1) / kTileSteps;
+  int csize = 1;
+  while (csize < 16 && groups * csize < 2 * a.num_sms && csize < tiles) csize *= 2;
+  const size_t smem = (size_t)stages * planes * kPlane + 1024 +
+                      (csize > 1 ? 2 * csize * 32 * sizeof(MapV<Word<E>::V>) : 0);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && csize > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * csize));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)csize;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, p);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return e;
+}
+
+// Stages of the ring: two tiles in flight a block.  A third leaves room for
+// two blocks an SM instead of three and measured slower (65536 x 1 x 1024
+// forward 158 -> 222 us, 512 x 128 x 1024 training 353 -> 386 us).
+template <typename E>
+cudaError_t forward_tiles(const ScanArgs& a, cudaStream_t st) {
+  return a.gate ? run_tiles<E>(scan_forward_tiles<E, true, 2>, a, 3, 2, st)
+                : run_tiles<E>(scan_forward_tiles<E, false, 3>, a, 2, 3, st);
+}
+template <typename E>
+cudaError_t backward_tiles(const ScanArgs& a, cudaStream_t st) {
+  return a.gate ? run_tiles<E>(scan_backward_tiles<E, true, 2>, a, 4, 2, st)
+                : run_tiles<E>(scan_backward_tiles<E, false, 2>, a, 3, 2, st);
+}
+
+template <typename E, int V>
+cudaError_t forward_steps(const ScanArgs& a, cudaStream_t st) {
+  const ScanP p = params(a, V);
+  const unsigned blocks = (unsigned)((p.vecs + kThreads - 1) / kThreads);
+  if (a.gate) scan_steps_kernel<E, V, true><<<blocks, kThreads, 0, st>>>(p);
+  else scan_steps_kernel<E, V, false><<<blocks, kThreads, 0, st>>>(p);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t scan_forward(const ScanArgs& a, cudaStream_t st) {
-  if (by_four(a))
+  const bool four = by_four(a);
+  if (a.T <= 8) {
+    if (four) return a.bf16 ? forward_steps<bf16, 4>(a, st) : forward_steps<float, 4>(a, st);
+    return a.bf16 ? forward_steps<bf16, 1>(a, st) : forward_steps<float, 1>(a, st);
+  }
+  if (by_tiles(a)) return a.bf16 ? forward_tiles<bf16>(a, st) : forward_tiles<float>(a, st);
+  if (four)
     return a.bf16 ? run<bf16, 4, 16, 8, false>(a, st) : run<float, 4, 16, 8, false>(a, st);
   return a.bf16 ? run<bf16, 1, 32, 16, false>(a, st) : run<float, 1, 32, 16, false>(a, st);
 }
 
 cudaError_t scan_backward(const ScanArgs& a, cudaStream_t st) {
+  if (by_tiles(a)) return a.bf16 ? backward_tiles<bf16>(a, st) : backward_tiles<float>(a, st);
   if (by_four(a))
     return a.bf16 ? run<bf16, 4, 16, 8, true>(a, st) : run<float, 4, 16, 4, true>(a, st);
   return a.bf16 ? run<bf16, 1, 32, 8, true>(a, st) : run<float, 1, 32, 8, true>(a, st);
