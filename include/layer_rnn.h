@@ -406,7 +406,8 @@ rnn_status_t rnn_debug_gemm_shape(int64_t M, int64_t N, int64_t K_total, int spl
  * conventions above hold: caller-owned dense row-major device memory, 16-byte
  * aligned, no overlap between arguments, asynchronous on `stream`, argument
  * errors before anything is enqueued, no allocation but the handle's 256-byte
- * status word at its first compute call.  RNN_F32: every tensor float32;
+ * status word at its first compute call (make one before capturing a CUDA
+ * graph).  RNN_F32: every tensor float32;
  * RNN_BF16: bfloat16; recurrent states (h0, hy, dhy, dh0) are float32 in
  * both.  Sums, states and gate arithmetic are float32 or more.
  * ========================================================================== */
@@ -484,9 +485,10 @@ rnn_status_t rnn_glu_backward(rnn_ops_t h, void* stream, int64_t M, int64_t K, i
  * ignored); scales [R, ceil(K / group)] of the handle's type; zeros the same
  * shape, bytes 0..15, or NULL = 8 everywhere.  group: 32, 64 or 128; any K up
  * to 65536 (the last group may be short); ldq (0: ceil(K / 2) rounded up to 16)
- * at least ceil(K / 2) and a multiple of 16.  Meant for few tokens (M up to 16
- * or so a pass over the weights; more run in passes of 16 at most).
- * Every group is summed in float32 before its scale.
+ * at least ceil(K / 2) and a multiple of 16.  Meant for few tokens: 16 of them a
+ * pass over the weights.
+ * Every group is summed in float32 before its scale.  A token with a value that
+ * is not finite has results that are not finite.
  * Errors: RNN_ERR_INVALID_ARG, RNN_ERR_MISALIGNED (bases; scales need 4 or 2
  * bytes, zeros 1), RNN_ERR_UNSUPPORTED (K > 65536, M, R of 2^31 and more). */
 rnn_status_t rnn_w4_matvec(rnn_ops_t h, void* stream, int64_t M, int64_t R, int64_t K, int group,

@@ -317,6 +317,7 @@ rnn_status_t rnn_w4_matvec(rnn_ops_t h, void* stream, int64_t M, int64_t R, int6
   a.x = x;
   a.y = y;
   a.num_sms = h->num_sms;
+  a.status = h->d_status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return finish(h, st, w4_matvec(a, st));
 }

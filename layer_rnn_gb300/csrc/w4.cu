@@ -3,24 +3,34 @@
 //   y[m][r] = sum_k x[m][k] (q[r][k] - zero[r][k / g]) scale[r][k / g]
 //
 // For a few tokens every weight is used a few times only, so the bytes of q
-// bound the product.  A warp streams blocks of 16 (or 32) rows by 256 weights,
-// 128 bytes a row, through its own ring of asynchronous copies, and multiplies
-// them on the tensor cores (m16n8k16, the rows as M, the tokens as N): with
-// one fused multiply-add a weight and token, the CUDA cores' conversions
-// alone would take as long as the bytes.  The order of k inside a product is
-// free, so the eight nibbles of a 32-bit word become operand pairs (k0, k4),
-// (k1, k5), ... by one shift, one mask and one subtraction each, and x is laid
-// out in shared memory to match.
+// bound the product, next to the instructions that unpack it: at the memory's
+// rate a scheduler has 46 cycles for 16 rows x 32 weights.  So:
+// - the tensor cores multiply (m16n8k16 in fp16, the rows as M, the tokens as
+//   N); fused multiply-adds would need a conversion a weight;
+// - a lane loads 16 bytes of a row, 32 weights, straight into the registers that
+//   become operands.  The order of k inside a product is free, so the eight
+//   nibbles of a word become the pairs (k0, k4), (k1, k5), (k2, k6), (k3, k7): five
+//   integer instructions and four fp16 ones, which also take the zero point off,
+//   exactly;
+// - no shared memory, barrier or address arithmetic for the weights: a ring
+//   of them (by TMA) took 24 more instructions for 16 x 32 weights, and the
+//   kernel 31 us where this one takes 21 (32768 x 4096, one token: 70 MB, 3.3 TB/s).  e4m3
+//   operands, into which nibbles turn with a mask, are converted to fp16 by the
+//   product itself here and saved nothing.
+// Where a group is 128 weights, the four lanes of a row take 32 of them each;
+// where it is smaller, they exchange words so that one product stays within a
+// group.
 //
-// Exactness: q - zero is a small whole number, exact in bf16 and fp16.  bf16
-// tokens are operands as they are.  float32 tokens become two fp16 columns,
-// x s = hi + lo 2^-11, s a power of two that maps the token's largest
-// magnitude below 2^14: 22 bits of every value near the largest.  Each group
-// is summed in float32 and only then multiplied by its scale.
+// Tokens lie in shared memory as fp16 columns in the same order, made once a
+// block: x s, s a power of two for every 128 values that maps the largest below
+// 2^14.  A bfloat16 token is one column (its 8 bits fit); a float32 one two,
+// x s = hi + lo 2^-11, 22 bits of every value near the largest.  Products are
+// exact; each group is summed in float32 and only then multiplied by its scale.
 //
-// The eight warps of a block share the rows and split K; blocks of a cluster
-// split it further where x would not fit shared memory or the rows alone do
-// not fill the card.  Partial sums are joined in a fixed order.
+// The four warps of a block take different rows, or, where the rows alone do not
+// fill the card, the same rows and different parts of K; blocks of a cluster
+// split K where it would not, or where x would not fit.  Partial sums are
+// joined in a fixed order.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -31,82 +41,53 @@
 namespace lr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kBlockK = 256;                 // weights of a row in one ring stage
-constexpr int kXBytes = 64 * 1024;           // x of one block at most
+constexpr int kBlockK = 128;        // weights of a row in one step
+constexpr int kTokens = 16;         // of a pass at most
+constexpr int kXBytes = 64 * 1024;  // x of one block at most; beyond half of it K is split sooner
 
 struct W4P {
-  int M, R, K, nkb, groups, tiles, tok;      // tok: tokens a pass
+  int M, R, K, nkb, groups, m0, toks;  // tokens m0 .. m0 + toks
   int64_t ldq;
   const void* x;
   const uint8_t* q;
   const void* scales;
   const uint8_t* zeros;
   void* y;
-  uint32_t x_bytes;                          // shared memory of x
+  int x_bytes;                         // shared memory of the columns
 };
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 bytes, or zeros where !ok (nothing is read then)
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
+
+// d = a b + d (d = a b where first, a constant once loops are unrolled)
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1, bool first) {
+  const float c0 = first ? 0.f : d[0], c1 = first ? 0.f : d[1], c2 = first ? 0.f : d[2],
+              c3 = first ? 0.f : d[3];
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-template <bool HALF>
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  if (HALF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// q - z of the eight nibbles of w as fp16 pairs (k0, k4), (k1, k5), (k2, k6),
+// (k3, k7).  A nibble under the exponent of 1024 is 1024 + q; there is room for
+// the second nibble of a byte in place, 1024 + 16 q, of which a sixteenth less
+// (64 + z) is q - z.  z1024, z64: 1024 + z and -(64 + z) in both halves.
+// (w & mask) | bits as one instruction; written as two operators it became two
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
+  return r;
 }
-
-// The eight nibbles of w less the zero point, as pairs (k0, k4), (k1, k5),
-// (k2, k6), (k3, k7).  zz: the zero point z in both halves, as the biased
-// value: bf16 128 + z (the nibble under the exponent of 128) or fp16 1024 + z.
-__device__ __forceinline__ void decode_bf16(uint32_t w, uint32_t zz, uint32_t (&a)[4]) {
-  const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162*>(&zz);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&v), z);
-    a[i] = *reinterpret_cast<const uint32_t*>(&d);
-  }
-}
-// fp16 has room for the second nibble of a byte in place: 1024 + 16 q, of
-// which a sixteenth less (64 + z) is q - z
-__device__ __forceinline__ void decode_f16(uint32_t w, uint32_t zz, uint32_t (&a)[4]) {
-  const __half2 z = *reinterpret_cast<const __half2*>(&zz);
-  const __half2 z64 = __hsub2(__float2half2_rn(960.f), z);  // -(64 + z)
+__device__ __forceinline__ void decode(uint32_t w, __half2 z1024, __half2 z64, uint32_t (&a)[4]) {
   const __half2 s = __float2half2_rn(0.0625f);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t lo = (w & 0x000F000Fu) | 0x64006400u, hi = (w & 0x00F000F0u) | 0x64006400u;
-    const __half2 d = __hsub2(*reinterpret_cast<__half2*>(&lo), z);
-    const __half2 e = __hfma2(*reinterpret_cast<__half2*>(&hi), s, z64);
+    const uint32_t lo = and_or(w, 0x000F000Fu, 0x64006400u), hi = and_or(w, 0x00F000F0u, 0x64006400u);
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&lo), z1024);
+    const __half2 e = __hfma2(*reinterpret_cast<const __half2*>(&hi), s, z64);
     a[2 * i] = *reinterpret_cast<const uint32_t*>(&d);
     a[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&e);
     w >>= 8;
@@ -136,296 +117,332 @@ __device__ __forceinline__ void st_rank0(float* local, float v) {
 // 2^e as a float, e within the normal range
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// F32: element type float32 (two columns a token), else bf16.  NT: column
-// tiles of 8; MT: row tiles of 16; GS: 32-weight chunks a group; ST: stages.
-template <bool F32, int NT, int MT, int GS, bool ZERO, int ST>
-__global__ void __launch_bounds__(kThreads) w4_kernel(const W4P p) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kRows = 16 * MT, kCols = 8 * NT;
-  constexpr int kStage = kRows * 128;               // bytes of a stage of one warp
-  constexpr int kGroups = 8 / GS;                   // groups of a block of 256 weights
-  constexpr int kHeld = kGroups > 4 ? 2 : 1;        // of them held by a lane
-  constexpr int kBufs = NT == 4 ? 1 : 2;            // of the joined partial sums
-  __shared__ float inv_scale[16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const unsigned csize = cl_size(), rank = cl_rank();
-  const int m0 = blockIdx.y * p.tok, toks = min(p.tok, p.M - m0);
-  const int cols = F32 ? 2 * toks : toks;
-  const int kb0 = (int)((int64_t)rank * p.nkb / csize), kb1 = (int)((int64_t)(rank + 1) * p.nkb / csize);
-  const int clusters = gridDim.x / csize, first = blockIdx.x / csize;
-  const int per = (kb1 - kb0 + kWarps - 1) / kWarps;  // blocks of a warp and tile
-  const int my_tiles = first < p.tiles ? (p.tiles - 1 - first) / clusters + 1 : 0;
-  const int items = my_tiles * per;
-  unsigned char* xs = smem;
-  unsigned char* ring = smem + p.x_bytes + warp * (ST * kStage);
-  float* red = reinterpret_cast<float*>(smem + p.x_bytes + kWarps * ST * kStage);
-  float* gather = red + kBufs * kWarps * kRows * kCols;  // clusters only: [2][csize][kRows * 16]
-  const uint32_t ring_at = smem_at(ring), xs_at = smem_at(xs);
+// word j of every lane of a quad to lane j: w[c] becomes lane c's word t
+__device__ __forceinline__ void transpose_quad(uint32_t (&w)[4], int t) {
+  // pairs at distance 1, then 2: each lane keeps the half it will own
+  const bool o1 = t & 1, o2 = t & 2;
+  uint32_t s0 = o1 ? w[0] : w[1], s1 = o1 ? w[2] : w[3];
+  s0 = __shfl_xor_sync(0xffffffffu, s0, 1);
+  s1 = __shfl_xor_sync(0xffffffffu, s1, 1);
+  if (o1) { w[0] = s0; w[2] = s1; } else { w[1] = s0; w[3] = s1; }
+  uint32_t r0 = o2 ? w[0] : w[2], r1 = o2 ? w[1] : w[3];
+  r0 = __shfl_xor_sync(0xffffffffu, r0, 2);
+  r1 = __shfl_xor_sync(0xffffffffu, r1, 2);
+  if (o2) { w[0] = r0; w[1] = r1; } else { w[2] = r0; w[3] = r1; }
+}
 
-  // scales (and zero points) of a stage: rows g and g + 8 of each row tile,
-  // groups t and t + 4
-  uint32_t sc[ST][MT][2][kHeld], zp[F32 && ZERO ? ST : 1][MT][2][kHeld];
-  int it_tile = first, it_kb = 0;  // of the next stage to load
-  auto issue = [&](int s) {
-    const int kb = kb0 + it_kb * kWarps + warp;
-    if (it_tile < p.tiles && kb < kb1) {
-      const int row0 = it_tile * kRows;
-#pragma unroll
-      for (int j = 0; j < 4 * MT; ++j) {
-        const int row = j * 4 + (lane >> 3), c = lane & 7;
-        const int64_t byte = (int64_t)kb * 128 + c * 16;
-        const bool ok = row0 + row < p.R && byte < p.ldq;
-        copy16(ring_at + s * kStage + row * 128 + ((c ^ (row & 7)) << 4),
-               p.q + (ok ? (int64_t)(row0 + row) * p.ldq + byte : 0), ok);
+// A warp makes one token's column(s) of 128 k, four values a lane, and its scale.
+// 16-byte piece (set j, lane quarter t) of a column holds k = 8 t + 32 j onwards
+// (DIRECT: 8 j + 32 t onwards), in the order k0 k4 k1 k5 k2 k6 k3 k7.
+struct Four { float v[4]; };
+template <bool F32>
+__device__ __forceinline__ Four get_four(const W4P& p, int kb, int m) {
+  const int k = kb * kBlockK + (threadIdx.x & 31) * 4;
+  const int64_t x0 = (int64_t)(p.m0 + m) * p.K + k;
+  Four r = {{0.f, 0.f, 0.f, 0.f}};
+  if (p.K % 4 == 0) {
+    if (k < p.K) {
+      if (F32) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + x0));
+        r.v[0] = q.x; r.v[1] = q.y; r.v[2] = q.z; r.v[3] = q.w;
+      } else {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(p.x) + x0));
+        r.v[0] = __uint_as_float(q.x << 16); r.v[1] = __uint_as_float(q.x & 0xffff0000u);
+        r.v[2] = __uint_as_float(q.y << 16); r.v[3] = __uint_as_float(q.y & 0xffff0000u);
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int u = 0; u < kHeld; ++u) {
-            const int row = row0 + mt * 16 + h * 8 + g, gi = kb * kGroups + u * 4 + t;
-            const bool ok = row < p.R && u * 4 + t < kGroups && gi < p.groups;
-            const int64_t at = (int64_t)row * p.groups + gi;
-            uint32_t sv = 0, zv = 8;
-            if (ok) {
-              sv = F32 ? __ldcs(static_cast<const unsigned*>(p.scales) + at)
-                       : (uint32_t)__ldcs(static_cast<const unsigned short*>(p.scales) + at);
-              if (ZERO) zv = __ldcs(p.zeros + at);
-            }
-            if (!F32 && ZERO) sv |= (0x4300u | zv) << 16;
-            sc[s][mt][h][u] = sv;
-            if (F32 && ZERO) zp[s][mt][h][u] = zv;
-          }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++it_kb == per) { it_kb = 0; it_tile += clusters; }
-  };
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) issue(s);
-
-  // x into shared memory: chunk of 32 k, column, lane t's eight values
-  // k0 k4 k1 k5 k2 k6 k3 k7 (t * 8 onwards)
-  const int k_from = kb0 * kBlockK, chunks = (kb1 - kb0) * (kBlockK / 32);
-  if (F32) {
-    const float* x = static_cast<const float*>(p.x) + (int64_t)m0 * p.K;
-    for (int m = warp; m < toks; m += kWarps) {
-      unsigned mx = 0;
-      const int k_to = min(p.K, kb1 * kBlockK);
-      for (int k = k_from + lane; k < k_to; k += 32)
-        mx = max(mx, __float_as_uint(x[(int64_t)m * p.K + k]) & 0x7fffffffu);
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      // infinities and NaN: no scale, the row's results are not finite
-      int e = mx >= 0x7f800000u || mx == 0 ? 0 : 13 - ((int)(mx >> 23) - 127);
-      e = min(max(e, -126), 126);
-      if (lane == 0) inv_scale[m] = exp2i(-e);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < chunks * toks * 4; i += kThreads) {
-      const int tt = i & 3, cm = i >> 2, m = cm % toks, c = cm / toks;
-      const float s = 1.0f / inv_scale[m];
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int k = k_from + c * 32 + tt * 8 + j + 4 * u;
-          v[u] = k < p.K ? x[(int64_t)m * p.K + k] * s : 0.f;
-        }
-        const __half2 h = __floats2half2_rn(v[0], v[1]);
-        const float2 hf = __half22float2(h);
-        const __half2 l = __floats2half2_rn(isinf(hf.x) ? 0.f : (v[0] - hf.x) * 2048.f,
-                                            isinf(hf.y) ? 0.f : (v[1] - hf.y) * 2048.f);
-        hi[j] = *reinterpret_cast<const uint32_t*>(&h);
-        lo[j] = *reinterpret_cast<const uint32_t*>(&l);
-      }
-      uint4* d = reinterpret_cast<uint4*>(xs) + (size_t)(c * cols + 2 * m) * 4 + tt;
-      d[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      d[4] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
   } else {
-    const unsigned short* x = static_cast<const unsigned short*>(p.x) + (int64_t)m0 * p.K;
-    for (int i = threadIdx.x; i < chunks * toks * 4; i += kThreads) {
-      const int tt = i & 3, cm = i >> 2, m = cm % toks, c = cm / toks;
-      uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = k_from + c * 32 + tt * 8 + j;
-        const uint32_t a = k < p.K ? x[(int64_t)m * p.K + k] : 0u;
-        const uint32_t b = k + 4 < p.K ? x[(int64_t)m * p.K + k + 4] : 0u;
-        v[j] = a | (b << 16);
+    for (int u = 0; u < 4; ++u)
+      if (k + u < p.K)
+        r.v[u] = F32 ? __ldg(static_cast<const float*>(p.x) + x0 + u)
+                     : __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(p.x) + x0 + u) << 16);
+  }
+  return r;
+}
+template <bool F32, bool DIRECT>
+__device__ __forceinline__ void make_columns(const Four& x, int m, unsigned char* at, int cols, float* mul) {
+  const int lane = threadIdx.x & 31;
+  const float (&v)[4] = x.v;
+  unsigned mx = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) mx = max(mx, __float_as_uint(v[u]) & 0x7fffffffu);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  const bool finite = mx < 0x7f800000u;
+  int e = finite && mx ? 13 - ((int)(mx >> 23) - 127) : 0;
+  e = min(max(e, -126), 126);
+  const float s = exp2i(e);
+  const int c = lane >> 3, q = (lane >> 1) & 3;  // 32-chunk, piece of it
+  unsigned char* to = at + (((DIRECT ? q : c) * cols + (F32 ? 2 * m : m)) * 4 + (DIRECT ? c : q)) * 16 +
+                      (lane & 1) * 8;
+  auto put = [&](const __half2 a, const __half2 b, unsigned char* d) {
+    // the even lane of a pair has k0..k3, the odd one k4..k7
+    const bool odd = lane & 1;
+    const uint32_t h01 = *reinterpret_cast<const uint32_t*>(&a), h23 = *reinterpret_cast<const uint32_t*>(&b);
+    const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? h01 : h23, 1);
+    const uint32_t lo = odd ? r : h01, hi = odd ? h23 : r;
+    *reinterpret_cast<uint2*>(d) = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+  };
+  const __half2 a = __floats2half2_rn(v[0] * s, v[1] * s), b = __floats2half2_rn(v[2] * s, v[3] * s);
+  put(a, b, to);
+  if (F32) {
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    put(__floats2half2_rn((v[0] * s - fa.x) * 2048.f, (v[1] * s - fa.y) * 2048.f),
+        __floats2half2_rn((v[2] * s - fb.x) * 2048.f, (v[3] * s - fb.y) * 2048.f), to + 64);
+  }
+  // a block that is not finite makes the token's results NaN
+  if (lane == 0) *mul = finite ? exp2i(-e) : __int_as_float(0x7fc00000);
+}
+
+// F32: element type float32 (two columns a token), else bf16.  NT: column
+// tiles of 8; MT: row tiles of 16 a warp; kWarps of a block; WK: of them, those
+// that split K (1 or all); GS: 32-weight chunks a group.
+template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
+__global__ void __launch_bounds__(32 * kWarps) w4_kernel(const W4P p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kThreads = 32 * kWarps;
+  constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
+  constexpr int D = MT == 1 ? 4 : 3;         // steps whose loads are under way
+  constexpr bool kDirect = GS == 4;
+  constexpr int kTok = F32 ? 1 : 2;          // tokens of a lane and column tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const unsigned csize = cl_size(), rank = cl_rank();
+  const int cols = F32 ? 2 * p.toks : p.toks;
+  const int block0 = (int)(blockIdx.x / csize) * kBlockRows;
+  const int row0 = block0 + (WK == 1 ? warp * kRows : 0);
+  const int kb0 = (int)((int64_t)rank * p.nkb / csize), kb1 = (int)((int64_t)(rank + 1) * p.nkb / csize);
+  const int first = kb0 + (WK == 1 ? 0 : warp);
+  const int steps = first < kb1 ? (kb1 - first + WK - 1) / WK : 0;
+  float* muls = reinterpret_cast<float*>(smem + p.x_bytes);  // [block of 128][kTokens]
+
+  // Nothing in the loop asks whether a row, a piece or a column exists: rows past
+  // the end read the last one's weights and columns past the last token the
+  // first's, whose sums are dropped; pieces past a row read its last, which
+  // meets x = 0.  Offsets are from the block's first row.
+  const uint8_t* wbase = p.q + (int64_t)block0 * p.ldq;
+  const char* sbase = static_cast<const char*>(p.scales) + (int64_t)block0 * p.groups * (F32 ? 4 : 2);
+  const uint8_t* zbase = p.zeros + (int64_t)block0 * p.groups;
+  uint32_t wo[MT][2], so[MT][2];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t row = (uint32_t)(min(row0 + mt * 16 + h * 8 + g, p.R - 1) - block0);
+      wo[mt][h] = row * (uint32_t)p.ldq;
+      so[mt][h] = row * (uint32_t)p.groups;
+    }
+  uint4 w[D][MT][2];
+  uint32_t sc[D][MT][2], zp[ZERO ? D : 1][MT][2];
+  auto fetch = [&](int slot, int i) {
+    if (i >= steps) return;
+    const int kb = first + i * WK;
+    const uint32_t piece = min((uint32_t)(kb * 64 + t * 16), (uint32_t)p.ldq - 16u);
+    // a block's 4 / GS groups: lane t has group t of them
+    const uint32_t gi = (uint32_t)min(kb * (4 / GS) + (GS == 4 ? 0 : GS == 2 ? (t & 1) : t), p.groups - 1);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[slot][mt][h] = __ldcs(reinterpret_cast<const uint4*>(wbase + (wo[mt][h] + piece)));
+        const uint32_t at = so[mt][h] + gi;
+        sc[slot][mt][h] = F32 ? __ldg(reinterpret_cast<const unsigned*>(sbase + (size_t)(at * 4u)))
+                              : (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(sbase + (size_t)(at * 2u)));
+        if (ZERO) zp[ZERO ? slot : 0][mt][h] = __ldg(zbase + at);
       }
-      reinterpret_cast<uint4*>(xs)[(size_t)(c * cols + m) * 4 + tt] = make_uint4(v[0], v[1], v[2], v[3]);
+  };
+#pragma unroll
+  for (int i = 0; i < D; ++i) fetch(i, i);
+
+  // x: eight loads of a warp under way at a time
+  constexpr int kBatch = 8;
+  const int pairs = (kb1 - kb0) * p.toks;
+  for (int e0 = warp; e0 < pairs; e0 += kBatch * kWarps) {
+    Four x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int e = min(e0 + j * kWarps, pairs - 1);
+      x[j] = get_four<F32>(p, kb0 + e / p.toks, e % p.toks);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int e = e0 + j * kWarps;
+      if (e >= pairs) break;
+      const int b = e / p.toks, m = e - b * p.toks;
+      make_columns<F32, kDirect>(x[j], m, smem + b * (cols * 256), cols, muls + b * kTokens + m);
     }
   }
   __syncthreads();
 
-  float fin[MT][NT][4];
+  float fin[MT][NT][2 * kTok];  // rows g and g + 8
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fin[mt][nt][i] = 0.f;
+      for (int i = 0; i < 2 * kTok; ++i) fin[mt][nt][i] = 0.f;
 
-  int tile = first, kbi = 0, par = 0;
-  for (int base = 0; base < items; base += ST) {
+  const unsigned char* xa[NT];
 #pragma unroll
-    for (int s = 0; s < ST; ++s) {
-      if (base + s >= items) break;
-      issue((s + ST - 1) % ST);
-      asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
-      __syncwarp();
-      const int kb = kb0 + kbi * kWarps + warp;
-      if (kb < kb1) {
-        const uint32_t st = ring_at + s * kStage + g * 128 + t * 4;
-        const uint32_t xa = xs_at + (uint32_t)((kb - kb0) * 8 * cols + g) * 64 + t * 16;
-        float acc[MT][NT][4];
-        float s0[MT], s1[MT];
-        uint32_t z0[MT], z1[MT];
+  for (int nt = 0; nt < NT; ++nt)
+    xa[nt] = smem + (first - kb0) * (cols * 256) + ((nt * 8 + g < cols ? nt * 8 + g : 0) * 4 + t) * 16;
+  const int x_chunk = cols * 64;
+  const float* ma = muls + (first - kb0) * kTokens + kTok * t;
+  for (int i0 = 0; i0 < steps; i0 += D) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c % GS == 0) {
-            const int gi = c / GS;
-            const int src = (lane & 28) | (gi & 3);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const uint32_t u0 = __shfl_sync(0xffffffffu, sc[s][mt][0][gi >> 2], src);
-              const uint32_t u1 = __shfl_sync(0xffffffffu, sc[s][mt][1][gi >> 2], src);
-              s0[mt] = __uint_as_float(F32 ? u0 : u0 << 16);
-              s1[mt] = __uint_as_float(F32 ? u1 : u1 << 16);
-              if (F32) {
-                z0[mt] = z1[mt] = 0x64086408u;
-                if (ZERO) {
-                  z0[mt] = 0x64006400u |
-                           __shfl_sync(0xffffffffu, zp[F32 && ZERO ? s : 0][mt][0][gi >> 2], src) * 0x10001u;
-                  z1[mt] = 0x64006400u |
-                           __shfl_sync(0xffffffffu, zp[F32 && ZERO ? s : 0][mt][1][gi >> 2], src) * 0x10001u;
-                }
-              } else {
-                z0[mt] = ZERO ? __byte_perm(u0, 0, 0x3232) : 0x43084308u;
-                z1[mt] = ZERO ? __byte_perm(u1, 0, 0x3232) : 0x43084308u;
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
-            }
-          }
-          uint4 b[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            b[nt] = make_uint4(0, 0, 0, 0);
-            if (nt * 8 + g < cols) b[nt] = lds128(xa + (uint32_t)(c * cols + nt * 8) * 64);
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint32_t at = st + mt * 2048 + ((c ^ g) << 4);
-            uint32_t a[4], d[4];
-            if (F32) {
-              decode_f16(lds32(at), z0[mt], a);
-              decode_f16(lds32(at + 1024), z1[mt], d);
-            } else {
-              decode_bf16(lds32(at), z0[mt], a);
-              decode_bf16(lds32(at + 1024), z1[mt], d);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<F32>(acc[mt][nt], a[0], d[0], a[1], d[1], b[nt].x, b[nt].y);
-              mma<F32>(acc[mt][nt], a[2], d[2], a[3], d[3], b[nt].z, b[nt].w);
-            }
-          }
-          if (c % GS == GS - 1) {
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                fin[mt][nt][0] = fmaf(s0[mt], acc[mt][nt][0], fin[mt][nt][0]);
-                fin[mt][nt][1] = fmaf(s0[mt], acc[mt][nt][1], fin[mt][nt][1]);
-                fin[mt][nt][2] = fmaf(s1[mt], acc[mt][nt][2], fin[mt][nt][2]);
-                fin[mt][nt][3] = fmaf(s1[mt], acc[mt][nt][3], fin[mt][nt][3]);
-              }
-          }
-        }
-      }
-      __syncwarp();
-      if (++kbi < per) continue;
-      // the tile is done: join the warps, then the blocks of the cluster
-      kbi = 0;
-      float* rw = red + (kBufs == 2 ? par : 0) * (kWarps * kRows * kCols);
-      if (kBufs == 1) __syncthreads();  // the last tile's sums have been read
+    for (int slot = 0; slot < D; ++slot) {
+      if (i0 + slot >= steps) break;
+      uint32_t a[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float* d = rw + (warp * kRows + mt * 16 + g) * kCols + nt * 8 + 2 * t;
-          *reinterpret_cast<float2*>(d) = make_float2(fin[mt][nt][0], fin[mt][nt][1]);
-          *reinterpret_cast<float2*>(d + 8 * kCols) = make_float2(fin[mt][nt][2], fin[mt][nt][3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) fin[mt][nt][i] = 0.f;
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = w[slot][mt][h];
+          a[mt][h][0] = v.x; a[mt][h][1] = v.y; a[mt][h][2] = v.z; a[mt][h][3] = v.w;
+          if (!kDirect) transpose_quad(a[mt][h], t);
         }
-      __syncthreads();
-      const int row0 = tile * kRows;
-      for (int i = threadIdx.x; i < kRows * toks; i += kThreads) {
-        const int row = i % kRows, m = i / kRows;
-        const float* d = rw + row * kCols + (F32 ? 2 * m : m);
-        float v = 0.f;
+      uint32_t zz[MT][2];  // 1024 + z in both halves, of this lane's group
+      if (ZERO)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          v += F32 ? fmaf(d[w * kRows * kCols + 1], 0x1p-11f, d[w * kRows * kCols])
-                   : d[w * kRows * kCols];
-        if (F32) v *= inv_scale[m];
-        if (csize > 1)
-          st_rank0(gather + (par * csize + rank) * (kRows * 16) + i, v);
-        else if (row0 + row < p.R) {
-          const int64_t at = (int64_t)(m0 + m) * p.R + row0 + row;
-          if (F32) static_cast<float*>(p.y)[at] = v;
-          else static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
-        }
-      }
-      if (csize > 1) {
-        cl_sync();
-        if (rank == 0)
-          for (int i = threadIdx.x; i < kRows * toks; i += kThreads) {
-            const int row = i % kRows, m = i / kRows;
-            float v = 0.f;
-            for (unsigned r = 0; r < csize; ++r) v += gather[(par * csize + r) * (kRows * 16) + i];
-            if (row0 + row < p.R) {
-              const int64_t at = (int64_t)(m0 + m) * p.R + row0 + row;
-              if (F32) static_cast<float*>(p.y)[at] = v;
-              else static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) zz[mt][h] = 0x64006400u | zp[ZERO ? slot : 0][mt][h] * 0x10001u;
+      float mul[NT][kTok];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int u = 0; u < kTok; ++u) mul[nt][u] = ma[nt * 4 * kTok + u];
+      float acc[MT][NT][4], s[MT][2];
+      __half2 z1024[MT][2], z64[MT][2];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c % GS == 0) {
+          const int src = (lane & 28) | (c / GS);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v = sc[slot][mt][h], z = 0x64086408u;
+              if (ZERO) z = zz[mt][h];
+              if (GS < 4) {
+                v = __shfl_sync(0xffffffffu, v, src);
+                if (ZERO) z = __shfl_sync(0xffffffffu, z, src);
+              }
+              s[mt][h] = __uint_as_float(F32 ? v : v << 16);
+              z1024[mt][h] = *reinterpret_cast<const __half2*>(&z);
+              z64[mt][h] = __hsub2(__float2half2_rn(960.f), z1024[mt][h]);
             }
+        }
+        uint4 b[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          b[nt] = *reinterpret_cast<const uint4*>(xa[nt] + c * x_chunk);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t u[4], d[4];
+          decode(a[mt][0][c], z1024[mt][0], z64[mt][0], u);
+          decode(a[mt][1][c], z1024[mt][1], z64[mt][1], d);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma(acc[mt][nt], u[0], d[0], u[1], d[1], b[nt].x, b[nt].y, c % GS == 0);
+            mma(acc[mt][nt], u[2], d[2], u[3], d[3], b[nt].z, b[nt].w, false);
           }
+        }
+        if (c % GS == GS - 1) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                  const float v = F32 ? fmaf(acc[mt][nt][2 * h + 1], 0x1p-11f, acc[mt][nt][2 * h])
+                                      : acc[mt][nt][2 * h + k];
+                  fin[mt][nt][h * kTok + k] =
+                      fmaf(s[mt][h] * mul[nt][k], v, fin[mt][nt][h * kTok + k]);
+                }
+        }
       }
-      par ^= 1;
-      tile += clusters;
+      fetch(slot, i0 + slot + D);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) xa[nt] += WK * 4 * x_chunk;
+      ma += WK * kTokens;
     }
+  }
+
+  auto put = [&](int row, int m, float v) {
+    if (row >= p.R) return;
+    const int64_t at = (int64_t)(p.m0 + m) * p.R + row;
+    if (F32) static_cast<float*>(p.y)[at] = v;
+    else static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
+  };
+  // joined sums: [block or warp][token][row].  Blocks of a cluster write theirs
+  // to block 0; warps that split K to their own block.
+  float* across = muls + (p.nkb + (int)csize - 1) / (int)csize * kTokens;
+  const int part = p.toks * kBlockRows;
+  float* within = across + (csize > 1 ? csize * part : 0);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < kTok; ++k) {
+          const int m = (nt * 4 + t) * kTok + k, r = (WK == 1 ? warp * kRows : 0) + mt * 16 + h * 8 + g;
+          const float v = fin[mt][nt][h * kTok + k];
+          if (m >= p.toks) continue;
+          if (WK > 1) within[warp * part + m * kBlockRows + r] = v;
+          else if (csize > 1) st_rank0(across + (int)rank * part + m * kBlockRows + r, v);
+          else put(block0 + r, m, v);
+        }
+  if (WK > 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < part; i += kThreads) {
+      float v = 0.f;
+#pragma unroll
+      for (int u = 0; u < kWarps; ++u) v += within[u * part + i];
+      if (csize > 1) st_rank0(across + (int)rank * part + i, v);
+      else put(block0 + i % kBlockRows, i / kBlockRows, v);
+    }
+  }
+  if (csize > 1) {
+    __syncwarp();
+    cl_sync();
+    if (rank == 0)
+      for (int i = threadIdx.x; i < part; i += kThreads) {
+        float v = 0.f;
+        for (unsigned c = 0; c < csize; ++c) v += across[c * part + i];
+        put(block0 + i % kBlockRows, i / kBlockRows, v);
+      }
   }
 }
 
-template <bool F32, int NT, int MT, int GS, bool ZERO>
-cudaError_t launch(W4P p, int csize, int num_sms, cudaStream_t st) {
-  constexpr int ST = MT == 1 ? 4 : 3;
-  auto kernel = w4_kernel<F32, NT, MT, GS, ZERO, ST>;
-  constexpr int kRows = 16 * MT;
-  p.tiles = (p.R + kRows - 1) / kRows;
-  const int cols = p.tok * (F32 ? 2 : 1);
-  p.x_bytes = (uint32_t)((p.nkb + csize - 1) / csize * 8 * cols * 64);
-  const size_t smem = p.x_bytes + kWarps * ST * kRows * 128 + (NT == 4 ? 1 : 2) * kWarps * kRows * 8 * NT * 4 +
-                      (csize > 1 ? 2 * csize * kRows * 16 * 4 : 0);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024);
+template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
+cudaError_t launch(W4P p, const W4Args& a, cudaStream_t st) {
+  auto kernel = w4_kernel<F32, NT, MT, kWarps, WK, GS, ZERO>;
+  constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
+  const int blocks = (p.R + kBlockRows - 1) / kBlockRows;
+  // K over the blocks of a cluster: until x fits, and until the card has two
+  // blocks an SM as long as each warp keeps four steps
+  const int cols = p.toks * (F32 ? 2 : 1);
+  auto x_of = [&](int c) { return (p.nkb + c - 1) / c * cols * 256; };
+  int c = 1;
+  while (c < 8 && x_of(c) > (kWarps == 8 ? kXBytes : kXBytes / 2)) c *= 2;
+  while (c < 8 && blocks * c < 2 * a.num_sms && p.nkb >= 8 * c * WK) c *= 2;
+  p.x_bytes = x_of(c);
+  const size_t smem = (size_t)p.x_bytes + (p.nkb + c - 1) / c * kTokens * 4 +
+                      (size_t)((c > 1 ? c : 0) + (WK > 1 ? kWarps : 0)) * p.toks * kBlockRows * 4;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
-  const int per_sm = std::max(1, (int)(220 * 1024 / (smem + 1024)));
-  const int clusters = std::min(p.tiles, std::max(1, num_sms * std::min(per_sm, 3) / csize));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * csize), (unsigned)((p.M + p.tok - 1) / p.tok));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(blocks * c));
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)csize;
+  at[0].val.clusterDim.x = (unsigned)c;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
@@ -434,17 +451,27 @@ cudaError_t launch(W4P p, int csize, int num_sms, cudaStream_t st) {
   return e;
 }
 
-template <bool F32, int NT, int MT>
-cudaError_t by_group(const W4P& p, int group, int csize, int num_sms, cudaStream_t st) {
-  const bool z = p.zeros != nullptr;
-  if (group == 32)
-    return z ? launch<F32, NT, MT, 1, true>(p, csize, num_sms, st)
-             : launch<F32, NT, MT, 1, false>(p, csize, num_sms, st);
-  if (group == 64)
-    return z ? launch<F32, NT, MT, 2, true>(p, csize, num_sms, st)
-             : launch<F32, NT, MT, 2, false>(p, csize, num_sms, st);
-  return z ? launch<F32, NT, MT, 4, true>(p, csize, num_sms, st)
-           : launch<F32, NT, MT, 4, false>(p, csize, num_sms, st);
+template <bool F32, int NT, int MT, int NW, int WK>
+cudaError_t by_group(const W4P& p, const W4Args& a, cudaStream_t st) {
+  const bool z = a.zeros != nullptr;
+  if (a.group == 32)
+    return z ? launch<F32, NT, MT, NW, WK, 1, true>(p, a, st)
+             : launch<F32, NT, MT, NW, WK, 1, false>(p, a, st);
+  if (a.group == 64)
+    return z ? launch<F32, NT, MT, NW, WK, 2, true>(p, a, st)
+             : launch<F32, NT, MT, NW, WK, 2, false>(p, a, st);
+  return z ? launch<F32, NT, MT, NW, WK, 4, true>(p, a, st)
+           : launch<F32, NT, MT, NW, WK, 4, false>(p, a, st);
+}
+
+// NW warps take different rows; four split K where rows in blocks of 16 MT NW, and
+// K split over clusters, would give the card less than two blocks an SM.
+template <bool F32, int NT, int MT, int NW>
+cudaError_t by_rows(const W4P& p, const W4Args& a, cudaStream_t st) {
+  const int64_t blocks =
+      (a.R + 16 * MT * NW - 1) / (16 * MT * NW) * std::max(1, std::min(8, p.nkb / 4));
+  return blocks >= 2 * a.num_sms ? by_group<F32, NT, MT, NW, 1>(p, a, st)
+                                 : by_group<F32, NT, 1, 4, 4>(p, a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -501,25 +528,24 @@ cudaError_t w4_matvec(const W4Args& a, cudaStream_t st) {
   p.groups = (int)((a.K + a.group - 1) / a.group);
   p.ldq = a.ldq;
   p.x = a.x; p.q = a.q; p.scales = a.scales; p.zeros = a.zeros; p.y = a.y;
-  const int per_tok = a.bf16 ? 1 : 2;
   // tokens a pass: as many as fit shared memory with K split over 8 blocks
-  p.tok = 16;
-  while (p.tok > 1 && (p.tok >= 2 * a.M ||
-                       (int64_t)((p.nkb + 7) / 8) * 8 * 64 * p.tok * per_tok > kXBytes))
-    p.tok /= 2;
-  p.tok = (int)std::min<int64_t>(p.tok, a.M);
-  const int cols = p.tok * per_tok;
-  int c = 1;
-  while (c < 8 && (int64_t)((p.nkb + c - 1) / c) * 8 * 64 * cols > kXBytes) c *= 2;
-  // few rows: split K as long as every warp keeps a block of 256 weights
-  while (c < 8 && (p.R + 15) / 16 * c < a.num_sms && p.nkb >= 2 * c * kWarps) c *= 2;
-  if (a.bf16) {
-    if (cols <= 8) return by_group<false, 1, 1>(p, a.group, c, a.num_sms, st);
-    return by_group<false, 2, 2>(p, a.group, c, a.num_sms, st);
+  int tok = kTokens;
+  while (tok > 1 && (int64_t)(p.nkb + 7) / 8 * 256 * tok * (a.bf16 ? 1 : 2) > kXBytes) tok /= 2;
+  for (int64_t m0 = 0; m0 < a.M; m0 += tok) {
+    p.m0 = (int)m0;
+    p.toks = (int)std::min<int64_t>(tok, a.M - m0);
+    cudaError_t e;
+    // two row tiles a warp where registers allow four blocks an SM with them; eight
+    // warps to a block's x where making its columns is a good part of the work
+    if (a.bf16)
+      e = p.toks <= 8 ? by_rows<false, 1, 2, 4>(p, a, st) : by_rows<false, 2, 1, 8>(p, a, st);
+    else
+      e = p.toks <= 4   ? by_rows<true, 1, 1, 4>(p, a, st)
+          : p.toks <= 8 ? by_rows<true, 2, 1, 8>(p, a, st)
+                        : by_rows<true, 4, 1, 8>(p, a, st);
+    if (e != cudaSuccess) return e;
   }
-  if (cols <= 8) return by_group<true, 1, 1>(p, a.group, c, a.num_sms, st);
-  if (cols <= 16) return by_group<true, 2, 2>(p, a.group, c, a.num_sms, st);
-  return by_group<true, 4, 2>(p, a.group, c, a.num_sms, st);
+  return cudaSuccess;
 }
 
 cudaError_t w4_quantize(const W4Args& a, const void* w, cudaStream_t st) {
