@@ -55,7 +55,7 @@ struct Maps {
   CUtensorMap a, b, out, dy;
 };
 
-template <int PROD>
+template <int PROD, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     glu_gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -108,11 +108,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
-    while (ok && walk_next(p, w, pairs)) {
+    while (ok && walk_next(p, w, pair, pairs)) {
       int z, mt, nt;
       tile_at(p, w.tile, z, mt, nt);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        if (!tc::mbar_wait_cluster_bounded(empty0 + 8 * s, ph, p.status, p.timeout_ns)) {
+        if (!wait_phase<false>(empty0 + 8 * s, ph, p.status)) {
           ok = false;
           break;
         }
@@ -148,15 +148,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0, n = 0;
     uint32_t ph = 0;
     bool ok = true;
-    while (ok && walk_next(p, w, pairs)) {
+    while (ok && walk_next(p, w, pair, pairs)) {
       const int buf = n & 1;
-      if (!tc::mbar_wait_cluster_bounded(tempty0 + 8 * buf, ((n >> 1) & 1) ^ 1u, p.status,
-                                         p.timeout_ns))
+      if (!wait_phase<false>(tempty0 + 8 * buf, ((n >> 1) & 1) ^ 1u, p.status))
         break;
       tc::fence_after();
       const uint32_t d = tmem + (uint32_t)(buf * 256);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        if (!tc::mbar_wait_cluster_bounded(full0 + 8 * s, ph, p.status, p.timeout_ns)) {
+        if (!wait_phase<false>(full0 + 8 * s, ph, p.status)) {
           ok = false;
           break;
         }
@@ -181,7 +180,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tempty = map_rank(tempty0, 0);
     uint32_t dy_ph = 0;
     int n = 0;
-    while (walk_next(p, w, pairs)) {
+    while (walk_next(p, w, pair, pairs)) {
       int z, mt, nt;
       tile_at(p, w.tile, z, mt, nt);
       const int buf = n & 1;
@@ -202,14 +201,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
-      if (!__all_sync(0xffffffffu, tc::mbar_wait_cluster_bounded(tfull0 + 8 * buf, (n >> 1) & 1,
-                                                                 p.status, p.timeout_ns)))
+      if (!__all_sync(0xffffffffu, wait_phase<false>(tfull0 + 8 * buf, (n >> 1) & 1, p.status)))
         break;
       tc::fence_after();
       ++n;
-      if (w.partial) {
+      if (w.slot >= 0) {
         // float32, 32 lanes x 4 columns a store, in the order the reduction reads
-        float4* d = part_at<kTile>(p, pair, w.slot, (int)rank * 4 + q) + lane;
+        float4* d = part_at<kTile>(p, w.slot, (int)rank * 4 + q) + lane;
 #pragma unroll 1
         for (int c = half * 128; c < half * 128 + 128; c += 32) {
           float v[32];
@@ -226,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (kGated) {
         if (PROD == kDgu && p.tma_dy) {
           if (!__all_sync(0xffffffffu,
-                          tc::mbar_wait_bounded(dy0 + 8 * e, dy_ph, p.status, p.timeout_ns)))
+                          wait_phase<false>(dy0 + 8 * e, dy_ph, p.status)))
             break;
           dy_ph ^= 1u;
         }
@@ -269,13 +267,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) {
               const int k = 8 * j + 2 * i;
               if (PROD == kForward) {
-                o[i] = glu::pack2(glu::value(g[k], p.act) * u[k], glu::value(g[k + 1], p.act) * u[k + 1]);
+                o[i] = glu::pack2(glu::value(g[k], ACT) * u[k], glu::value(g[k + 1], ACT) * u[k + 1]);
               } else {
                 const uint32_t dw = i == 0 ? dv.x : i == 1 ? dv.y : i == 2 ? dv.z : dv.w;
                 const float y0 = __uint_as_float(dw << 16), y1 = __uint_as_float(dw & 0xffff0000u);
                 float v0, d0, v1, d1;
-                glu::value_slope(g[k], p.act, v0, d0);
-                glu::value_slope(g[k + 1], p.act, v1, d1);
+                glu::value_slope(g[k], ACT, v0, d0);
+                glu::value_slope(g[k + 1], ACT, v1, d1);
                 o[i] = glu::pack2(y0 * u[k] * d0, y1 * u[k + 1] * d1);
                 o2[i] = glu::pack2(y0 * v0, y1 * v1);
               }
@@ -365,16 +363,15 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const unsigned short* __r
   }
 }
 
-template <int PROD>
-cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
-  auto kernel = glu_gemm_kernel<PROD>;
+template <int PROD, int ACT>
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+  auto kernel = glu_gemm_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = plan_pairs(&p, a.num_sms, 24);  // 256 KB each way
   // few row tiles walked together keep their rows of A in L2 beside all of B
   p.group = std::min(p.m_tiles, 16);
   p.status = a.status;
-  p.timeout_ns = 2000000000LL;
   kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   e = cudaGetLastError();
@@ -383,6 +380,14 @@ cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
   glu_join_kernel<bf16, kTile><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError();
+}
+template <int PROD>
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
+  if constexpr (PROD == kForward || PROD == kDgu) {
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
+  }
+  return launch_act<PROD, 2>(maps, p, a, st);
 }
 
 // x and W with rows that TMA can read: as they are, or copied
@@ -437,7 +442,6 @@ cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st) {
   p.planes = 1;
   p.nkb = (int)ceil_div(a.K, 64);
   p.rows = (int)a.M; p.cols = (int)a.F;
-  p.act = a.act;
   p.out = a.y; p.ld_out = a.F;
   return launch<kForward>(maps, p, a, st);
 }
@@ -464,8 +468,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.planes = 1;
     p.nkb = (int)ceil_div(a.K, 64);
     p.rows = (int)a.M; p.cols = (int)a.F;
-    p.act = a.act;
-    p.dy = a.dy; p.ld_dy = a.F;
+      p.dy = a.dy; p.ld_dy = a.F;
     e = launch<kDgu>(maps, p, a, st);
     if (e != cudaSuccess) return e;
   }

@@ -7,12 +7,15 @@
 namespace lr {
 namespace glu {
 
-// s = sigmoid(a), i = 1 - s, both to a few ulp (e held below 2^120 so that
-// e s stays 1 for very negative a; NaN goes through)
+// s = sigmoid(a), i = 1 - s, both to a few ulp: e = e^-a held below 2^120 so that
+// e s stays 1 for very negative a; NaN goes through.  The exponential and the
+// reciprocal that flush denormals: the others take eight more instructions,
+// and the epilogue of the backward product would not fit beside its MMAs.
 __device__ __forceinline__ void sigmoid_pair(float a, float& s, float& i) {
-  float e = __expf(-a);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
   asm("min.NaN.f32 %0, %0, 0f7B800000;" : "+f"(e));
-  s = __fdividef(1.0f, 1.0f + e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
   i = e * s;
 }
 

@@ -9,15 +9,16 @@
 // The sums need more than that.  The tensor core cuts off what does not fit
 // when it adds to its float32 accumulator; over a contraction of 1000 that
 // pulled results towards zero by 1.3e-5, ten times a float32 product's error.
-// So hi hi goes to an accumulator that holds 64 k at a time, four MMAs; the
-// epilogue warps add it to sums in registers, rounding to nearest, while the
-// MMAs fill another.  The small products, 2^-11 of it, keep one accumulator
-// each tile.  Tensor memory: two accumulators of 128 columns for hi hi, two for
-// the rest (this tile's and the next one's).
+// So hi hi goes to an accumulator that holds 64 k at a time, four MMAs; while the
+// eight MMAs of the small products follow, the epilogue warps add it to sums in
+// registers, rounding to nearest.  The small products, 2^-11 of it, keep one
+// accumulator each tile.  (256 columns each: all of tensor memory.)
 //
-// A pair of blocks works on 256 x 128 of a result (forward and dgu: 64
-// features).  Bound by the tensor cores at three passes a product; adding up
-// takes a third of that time beside them.  Every wait is bounded.
+// A pair of blocks works on 256 x 256 of a result (forward and dgu: 128
+// features).  Bound by the tensor cores at three passes a product.  Tiles 128
+// wide took 2.5 times as long: an operand byte then serves half as many
+// products, and shared memory bounds them, and there are twice as many
+// exchanges between the MMAs and the warps that add up.  Every wait is bounded.
 #include <cuda_fp16.h>
 
 #include "gemm.h"
@@ -28,11 +29,11 @@ namespace {
 
 using namespace glu;
 
-constexpr int kCols = 128;             // columns of a pair's tile
+constexpr int kCols = 256;             // columns of a pair's tile
 constexpr int kA = kHalf * 128;        // bytes: a block's rows, 64 k, hi or lo
-constexpr int kB = 64 * 128;           // a block's half of the columns
+constexpr int kB = kHalf * 128;        // a block's half of the columns
 constexpr int kStage = 2 * (kA + kB);
-constexpr int ST = 4;
+constexpr int ST = 3;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kSmem = ST * kStage + 1024;
@@ -49,13 +50,13 @@ __device__ __forceinline__ float unscale(unsigned mb) {
   return __int_as_float((127 - s) << 23);
 }
 
-template <int PROD>
+template <int PROD, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     glu_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   constexpr bool kAmn = PROD == kDw, kBmn = PROD == kDx || PROD == kDw;
   constexpr bool kGated = PROD == kForward || PROD == kDgu;
-  // kind::f16, fp16 operands, float32 sums, M = 256, N = 128
+  // kind::f16, fp16 operands, float32 sums, M = 256, N = 256
   constexpr uint32_t kIdesc = (1u << 4) | ((kAmn ? 1u : 0u) << 15) | ((kBmn ? 1u : 0u) << 16) |
                               ((uint32_t)(kCols >> 3) << 17) | ((uint32_t)(2 * kHalf >> 4) << 24);
   __shared__ __align__(8) uint64_t bars[2 * ST + 4];
@@ -98,11 +99,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0;
     uint32_t ph = 1;
     bool ok = true;
-    while (ok && walk_next(p, w, pairs)) {
+    while (ok && walk_next(p, w, pair, pairs)) {
       int z, mt, nt;
       tile_at(p, w.tile, z, mt, nt);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        if (!tc::mbar_wait_cluster_bounded(empty0 + 8 * s, ph, p.status, p.timeout_ns)) {
+        if (!wait_phase<false>(empty0 + 8 * s, ph, p.status)) {
           ok = false;
           break;
         }
@@ -114,18 +115,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const CUtensorMap* ma = h ? &maps.al : &maps.ah;
           const CUtensorMap* mb = h ? &maps.bl : &maps.bh;
           const uint32_t at = a + h * kA, bt = b + h * kB;
+          const int n0 = nt * kCols + (int)rank * kHalf;
           if (kGated) {
             load_box(at, ma, kb * 64, mt * 2 * kHalf + (int)rank * kHalf, 0, bar);
-            load_box(bt, mb, kb * 64, nt * 64, (int)rank, bar);
+            load_box(bt, mb, kb * 64, nt * kHalf, (int)rank, bar);
           } else if (PROD == kDx) {
             const int pl = kb >= p.kb_plane, k = (kb - pl * p.kb_plane) * 64;
             load_box(at, ma, k, mt * 2 * kHalf + (int)rank * kHalf, pl, bar);
-            load_box(bt, mb, nt * kCols + (int)rank * 64, k, pl, bar);
+            load_box(bt, mb, n0, k, pl, bar);
+            load_box(bt + 8192, mb, n0 + 64, k, pl, bar);
           } else {
             const int f0 = mt * 2 * kHalf + (int)rank * kHalf;
             load_box(at, ma, f0, kb * 64, z, bar);
             load_box(at + 8192, ma, f0 + 64, kb * 64, z, bar);
-            load_box(bt, mb, nt * kCols + (int)rank * 64, kb * 64, 0, bar);
+            load_box(bt, mb, n0, kb * 64, 0, bar);
+            load_box(bt + 8192, mb, n0 + 64, kb * 64, 0, bar);
           }
         }
         if (++s == ST) { s = 0; ph ^= 1u; }
@@ -141,39 +145,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int s = 0, blk = 0, n = 0;
     uint32_t ph = 0;
     bool ok = true;
-    while (ok && walk_next(p, w, pairs)) {
-      const uint32_t d1 = tmem + 256u + (uint32_t)((n & 1) * kCols);
+    auto step = [](int kk, bool mn) { return (uint64_t)(kk * (mn ? 128 : 2)); };
+    while (ok && walk_next(p, w, pair, pairs)) {
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
-        const int buf = blk & 1;
-        if (!tc::mbar_wait_cluster_bounded(tempty0 + 8 * buf, ((blk >> 1) & 1) ^ 1u, p.status,
-                                           p.timeout_ns) ||
-            !tc::mbar_wait_cluster_bounded(full0 + 8 * s, ph, p.status, p.timeout_ns)) {
-          ok = false;
-          break;
-        }
+        ok = wait_phase<false>(tempty0, (blk & 1) ^ 1u, p.status) &&
+             wait_phase<false>(full0 + 8 * s, ph, p.status);
+        if (!ok) break;
         tc::fence_after();
         const uint32_t a = base + (uint32_t)(s * kStage), b = a + 2 * kA;
         const uint64_t ah = operand_desc<kAmn>(a), al = operand_desc<kAmn>(a + kA);
         const uint64_t bh = operand_desc<kBmn>(b), bl = operand_desc<kBmn>(b + kB);
-        const uint32_t d0 = tmem + (uint32_t)(buf * kCols);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma2(tmem, ah + step(kk, kAmn), bh + step(kk, kBmn), kIdesc, kk > 0 ? 1u : 0u);
+        commit2(tfull0);
+        if (kb == w.kb0) {
+          ok = wait_phase<false>(tempty0 + 8, (n & 1) ^ 1u, p.status);
+          if (!ok) break;
+          tc::fence_after();
+        }
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t sa = (uint64_t)(kk * (kAmn ? 128 : 2)), sb = (uint64_t)(kk * (kBmn ? 128 : 2));
-          mma2(d0, ah + sa, bh + sb, kIdesc, kk > 0 ? 1u : 0u);
-          mma2(d1, ah + sa, bl + sb, kIdesc, (kb > w.kb0 || kk > 0) ? 1u : 0u);
-          mma2(d1, al + sa, bh + sb, kIdesc, 1u);
+          mma2(tmem + kCols, ah + step(kk, kAmn), bl + step(kk, kBmn), kIdesc,
+               (kb > w.kb0 || kk > 0) ? 1u : 0u);
+          mma2(tmem + kCols, al + step(kk, kAmn), bh + step(kk, kBmn), kIdesc, 1u);
         }
         commit2(empty0 + 8 * s);
-        commit2(tfull0 + 8 * buf);
         if (++s == ST) { s = 0; ph ^= 1u; }
       }
+      if (ok) commit2(tfull0 + 8);
       ++n;
     }
   } else if (warp >= 2) {
-    // warp e adds up rows 32 (warp % 4).. of two runs of 32 columns: where gate
+    // warp e adds up rows 32 (warp % 4).. of two runs of 64 columns: where gate
     // and up columns belong together, the same features of both
     const int e = warp - 2, q = warp & 3, half = e >> 2;
-    const int c0 = kGated ? 32 * half : 64 * half, c1 = kGated ? 64 + 32 * half : 64 * half + 32;
+    const int c0 = kGated ? 64 * half : 128 * half, c1 = kGated ? 128 + 64 * half : 128 * half + 64;
     const uint32_t tempty = map_rank(tempty0, 0);
     const float ia = unscale(*p.amax), ib = unscale(*p.bmax);
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -181,47 +188,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     unsigned mx = 0;
     int blk = 0, n = 0;
     bool ok = true;
-    while (ok && walk_next(p, w, pairs)) {
+    while (ok && walk_next(p, w, pair, pairs)) {
       __syncwarp();  // rows past the end skip their stores
       int z, mt, nt;
       tile_at(p, w.tile, z, mt, nt);
-      float s0[32], s1[32];
+      float s0[64], s1[64];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s0[i] = s1[i] = 0.f;
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
-        const int buf = blk & 1;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait_cluster_bounded(
-                                         tfull0 + 8 * buf, (blk >> 1) & 1, p.status, p.timeout_ns))) {
-          ok = false;
-          break;
-        }
-        tc::fence_after();
-        float v[32];
-        tc::tmem_ld32(lanes + (uint32_t)(buf * kCols + c0), v);
+      for (int i = 0; i < 64; ++i) s0[i] = s1[i] = 0.f;
+      auto add = [&](uint32_t d) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s0[i] += v[i];
-        tc::tmem_ld32(lanes + (uint32_t)(buf * kCols + c1), v);
+        for (int h = 0; h < 2; ++h) {
+          float v[32];
+          tc::tmem_ld32(d + (uint32_t)(c0 + 32 * h), v);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s1[i] += v[i];
-        if (kb == w.kb1 - 1) {  // the small products, before the next tile's may begin
-          const uint32_t d1 = lanes + 256u + (uint32_t)((n & 1) * kCols);
-          tc::tmem_ld32(d1 + (uint32_t)c0, v);
+          for (int i = 0; i < 32; ++i) s0[32 * h + i] += v[i];
+          tc::tmem_ld32(d + (uint32_t)(c1 + 32 * h), v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s0[i] = (s0[i] + v[i]) * ia * ib;
-          tc::tmem_ld32(d1 + (uint32_t)c1, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s1[i] = (s1[i] + v[i]) * ia * ib;
+          for (int i = 0; i < 32; ++i) s1[32 * h + i] += v[i];
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at(tempty + 8 * buf);
+      };
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        const bool got = wait_phase<false>(bar, parity, p.status);
+        tc::fence_after();
+        return (bool)__all_sync(0xffffffffu, got);
+      };
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
+        ok = wait(tfull0, blk & 1);
+        if (!ok) break;
+        add(lanes);
+        if (lane == 0) arrive_at(tempty);
       }
-      if (!ok) break;
+      if (ok) ok = wait(tfull0 + 8, n & 1);
+      if (ok) {
+        add(lanes + kCols);
+        if (lane == 0) arrive_at(tempty + 8);
+      }
       ++n;
-      if (w.partial) {
-        float4* d = part_at<kCols>(p, pair, w.slot, (int)rank * 4 + q) + lane;
+      if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 64; ++i) {
+        s0[i] = s0[i] * ia * ib;
+        s1[i] = s1[i] * ia * ib;
+      }
+      if (w.slot >= 0) {
+        float4* d = part_at<kCols>(p, w.slot, (int)rank * 4 + q) + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
           __stcs(d + (c0 / 4 + i) * 32, make_float4(s0[4 * i], s0[4 * i + 1], s0[4 * i + 2], s0[4 * i + 3]));
           __stcs(d + (c1 / 4 + i) * 32, make_float4(s1[4 * i], s1[4 * i + 1], s1[4 * i + 2], s1[4 * i + 3]));
         }
@@ -229,51 +243,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const int row = mt * 2 * kHalf + (int)rank * kHalf + q * 32 + lane;
       if (row >= p.rows) continue;
-      if (kGated) {
-        const int f0 = nt * 64 + half * 32;
-        if (PROD == kForward) {
+      auto put = [&](const float (&v)[64], int plane, int col) {
+        float* o = static_cast<float*>(p.out) + ((int64_t)plane * p.rows + row) * p.ld_out + col;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s0[i] = value(s0[i], p.act) * s1[i];
-        } else {
-          const float* dy = static_cast<const float*>(p.dy) + (int64_t)row * p.ld_dy + f0;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float v, d;
-            value_slope(s0[i], p.act, v, d);
-            const float y = f0 + i < p.cols ? __ldg(dy + i) : 0.f;
-            s0[i] = y * s1[i] * d;
-            s1[i] = y * v;
-            mx = max(mx, max(__float_as_uint(s0[i]) & 0x7fffffffu, __float_as_uint(s1[i]) & 0x7fffffffu));
-          }
+        for (int i = 0; i < 16; ++i) {
+          const float f[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+          if (vec && col + 4 * i < p.cols) store4(o + 4 * i, f);
+          if (!vec)
+            for (int u = 0; u < 4; ++u)
+              if (col + 4 * i + u < p.cols) o[4 * i + u] = f[u];
         }
+      };
+      if (!kGated) {
+        put(s0, z, nt * kCols + c0);
+        put(s1, z, nt * kCols + c1);
+        continue;
+      }
+      const int f0 = nt * kHalf + half * 64;
+      if (PROD == kForward) {
 #pragma unroll
-        for (int pl = 0; pl < (PROD == kDgu ? 2 : 1); ++pl) {
-          float* o = static_cast<float*>(p.out) + ((int64_t)pl * p.rows + row) * p.ld_out + f0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float v[4] = {pl ? s1[4 * i] : s0[4 * i], pl ? s1[4 * i + 1] : s0[4 * i + 1],
-                                pl ? s1[4 * i + 2] : s0[4 * i + 2], pl ? s1[4 * i + 3] : s0[4 * i + 3]};
-            if (vec && f0 + 4 * i < p.cols) store4(o + 4 * i, v);
-            if (!vec)
-              for (int u = 0; u < 4; ++u)
-                if (f0 + 4 * i + u < p.cols) o[4 * i + u] = v[u];
-          }
-        }
+        for (int i = 0; i < 64; ++i) s0[i] = value(s0[i], ACT) * s1[i];
+        put(s0, 0, f0);
       } else {
+        const float* dy = static_cast<const float*>(p.dy) + (int64_t)row * p.ld_dy + f0;
+        const bool dvec = p.tma_dy != 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = nt * kCols + (h ? c1 : c0);
-          float* o = static_cast<float*>(p.out) + ((int64_t)z * p.rows + row) * p.ld_out + col;
+        for (int i = 0; i < 16; ++i) {
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (dvec) {
+            if (f0 + 4 * i < p.cols) y = __ldg(reinterpret_cast<const float4*>(dy + 4 * i));
+          } else {
+            if (f0 + 4 * i < p.cols) y.x = __ldg(dy + 4 * i);
+            if (f0 + 4 * i + 1 < p.cols) y.y = __ldg(dy + 4 * i + 1);
+            if (f0 + 4 * i + 2 < p.cols) y.z = __ldg(dy + 4 * i + 2);
+            if (f0 + 4 * i + 3 < p.cols) y.w = __ldg(dy + 4 * i + 3);
+          }
+          const float yv[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float v[4] = {h ? s1[4 * i] : s0[4 * i], h ? s1[4 * i + 1] : s0[4 * i + 1],
-                                h ? s1[4 * i + 2] : s0[4 * i + 2], h ? s1[4 * i + 3] : s0[4 * i + 3]};
-            if (vec && col + 4 * i < p.cols) store4(o + 4 * i, v);
-            if (!vec)
-              for (int u = 0; u < 4; ++u)
-                if (col + 4 * i + u < p.cols) o[4 * i + u] = v[u];
+          for (int u = 0; u < 4; ++u) {
+            float v, d;
+            value_slope(s0[4 * i + u], ACT, v, d);
+            s0[4 * i + u] = yv[u] * s1[4 * i + u] * d;
+            s1[4 * i + u] = yv[u] * v;
+            mx = max(mx, max(__float_as_uint(s0[4 * i + u]) & 0x7fffffffu,
+                             __float_as_uint(s1[4 * i + u]) & 0x7fffffffu));
           }
         }
+        put(s0, 0, f0);
+        put(s1, 1, f0);
       }
     }
     if (PROD == kDgu) {
@@ -291,16 +308,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  : "memory");
 }
 
-template <int PROD>
-cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
-  auto kernel = glu_f32_kernel<PROD>;
+template <int PROD, int ACT>
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+  auto kernel = glu_f32_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  const int pairs = plan_pairs(&p, a.num_sms, 16);  // 128 KB each way
+  const int pairs = plan_pairs(&p, a.num_sms, 8);  // 256 KB each way, three products a block
   p.group = std::min(p.m_tiles, 16);
   p.tma_out = p.ld_out % 4 == 0 && p.cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   p.status = a.status;
-  p.timeout_ns = 2000000000LL;
   kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   e = cudaGetLastError();
@@ -309,6 +325,14 @@ cudaError_t launch(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
   glu_join_kernel<float, kCols><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return cudaGetLastError();
+}
+template <int PROD>
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
+  if constexpr (PROD == kForward || PROD == kDgu) {
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
+  }
+  return launch_act<PROD, 2>(maps, p, a, st);
 }
 
 struct Pairs {
@@ -361,18 +385,17 @@ cudaError_t operands(const GluArgs& a, unsigned* mx, const Pairs& x, const Pairs
 bool gated_maps(const GluArgs& a, const Pairs& x, const Pairs& w, Maps* m) {
   return map3(&m->ah, x.hi, a.K, a.M, 1, x.ld, a.M, 128) &&
          map3(&m->al, x.lo, a.K, a.M, 1, x.ld, a.M, 128) &&
-         map3(&m->bh, w.hi, a.K, a.F, 2, w.ld, a.F, 64) &&
-         map3(&m->bl, w.lo, a.K, a.F, 2, w.ld, a.F, 64);
+         map3(&m->bh, w.hi, a.K, a.F, 2, w.ld, a.F, 128) &&
+         map3(&m->bl, w.lo, a.K, a.F, 2, w.ld, a.F, 128);
 }
 
 P gated(const GluArgs& a, const unsigned* mx) {
   P p = {};
   p.m_tiles = (int)ceil_div(a.M, 2 * kHalf);
-  p.n_tiles = (int)ceil_div(a.F, 64);
+  p.n_tiles = (int)ceil_div(a.F, kHalf);
   p.planes = 1;
   p.nkb = (int)ceil_div(a.K, 64);
   p.rows = (int)a.M; p.cols = (int)a.F;
-  p.act = a.act;
   p.amax = mx; p.bmax = mx + 1;
   return p;
 }
@@ -412,6 +435,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     if (!gated_maps(a, x, w, &maps)) return cudaErrorInvalidValue;
     P p = gated(a, mx);
     p.dy = a.dy; p.ld_dy = a.F;
+    p.tma_dy = a.F % 4 == 0;
     p.out = dgu; p.ld_out = Fp;
     p.omax = mx + 2;
     TRY(launch<kDgu>(maps, p, a, st));

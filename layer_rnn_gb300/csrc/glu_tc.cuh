@@ -10,7 +10,7 @@
 
 #include "glu.cuh"
 #include "ops.h"
-#include "tc_common.cuh"
+#include "wait.cuh"
 
 namespace lr {
 namespace glu {
@@ -22,10 +22,10 @@ enum Product { kForward = 0, kDgu = 1, kDx = 2, kDw = 3 };
 struct P {
   int m_tiles, n_tiles, planes;  // tiles of a plane of the result; planes (kDw: 2)
   int nkb, kb_plane;             // 64-element blocks of the contraction; per plane (kDx)
-  int whole;                     // tiles done whole, in turn; the rest is cut evenly
+  int whole;                     // tiles done whole, in turn; the rest is cut
+  int head;                      // blocks of a cut tile that one pair does first
   int rows, cols;                // of a plane of the result
   int group;                     // row tiles walked together (reuse in L2)
-  int act;
   int tma_out, tma_dy;
   void* out;                     // plain stores: row pitch ld_out, planes `rows` rows apart
   int64_t ld_out;
@@ -36,7 +36,6 @@ struct P {
   const unsigned* bmax;          // magnitudes (float bit patterns)
   unsigned* omax;                // kDgu: that of the result
   int* status;
-  long long timeout_ns;
 };
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, unsigned rank) {
@@ -80,9 +79,11 @@ __device__ __forceinline__ void commit2(uint32_t bar) {
       "h"((unsigned short)3)
       : "memory");
 }
+// Arrive on a barrier of either block.  What it orders is reads of tensor memory
+// (tcgen05.fence before it), not stores: a release at cluster scope would wait for
+// the thread's stores as well, 3000 cycles at times.
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // operand tile of 128 rows (or columns) x 64 k, 128-byte swizzle.  K-major:
@@ -99,37 +100,64 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
   return d;
 }
 
-// What a pair works on, in order.  pos walks the evenly cut part.
+// What a pair works on, in order: whole tiles in turn, then its share of the
+// `left` tiles that are cut along the contraction.  Pair r < left takes the first
+// `head` blocks of cut tile r; the other pairs share the tiles' ends, laid end to
+// end, evenly.  (Heads run side by side through the same part of the contraction
+// and share its operands in L2.  Cutting all of it evenly instead had every pair
+// in another part: dW of 65536 x 1024 x 4096 read 3.4 GB that way.)
 struct Walk {
   int tile, kb0, kb1;
-  bool partial;
-  int slot;
-  int64_t pos, from, to;
+  int slot;          // of the partial sums, or -1: the whole tile
+  int64_t pos, to;   // in the ends; heads: pos = -1, done: pos = to
 };
-__device__ __forceinline__ int64_t cut(const P& p, int64_t pair, int64_t pairs) {
-  const int64_t left = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
-  return pair * (left * p.nkb) / pairs;
-}
+struct Cut {
+  int left, ends;    // cut tiles; blocks of an end
+  __device__ __forceinline__ explicit Cut(const P& p)
+      : left(p.m_tiles * p.n_tiles * p.planes - p.whole), ends(p.nkb - p.head) {}
+  // where tail pair j (pair left + j) begins
+  __device__ __forceinline__ int64_t begin(int64_t j, int pairs) const {
+    return pairs > left ? j * ((int64_t)left * ends) / (pairs - left) : 0;
+  }
+};
 __device__ __forceinline__ void walk_start(const P& p, Walk& w, int pair, int pairs) {
   w.tile = pair - pairs;
-  w.from = w.pos = cut(p, pair, pairs);
-  w.to = cut(p, pair + 1, pairs);
+  const Cut c(p);
+  w.pos = w.to = 0;
+  if (c.left == 0) return;
+  if (pair < c.left) {
+    w.pos = -1;
+  } else {
+    w.pos = c.begin(pair - c.left, pairs);
+    w.to = c.begin(pair - c.left + 1, pairs);
+  }
 }
-__device__ __forceinline__ bool walk_next(const P& p, Walk& w, int pairs) {
+__device__ __forceinline__ bool walk_next(const P& p, Walk& w, int pair, int pairs) {
   if (w.tile + pairs < p.whole) {
     w.tile += pairs;
     w.kb0 = 0;
     w.kb1 = p.nkb;
-    w.partial = false;
+    w.slot = -1;
+    return true;
+  }
+  w.tile = p.whole;  // whole tiles are done
+  const Cut c(p);
+  if (w.pos < 0) {
+    w.tile = p.whole + pair;
+    w.kb0 = 0;
+    w.kb1 = p.head;
+    w.slot = pair;
+    w.pos = w.to = 0;
     return true;
   }
   if (w.pos >= w.to) return false;
-  w.tile = p.whole + (int)(w.pos / p.nkb);
-  w.kb0 = (int)(w.pos % p.nkb);
-  w.kb1 = (int)min((int64_t)p.nkb, w.kb0 + (w.to - w.pos));
-  w.partial = w.kb1 - w.kb0 < p.nkb;
-  w.slot = w.pos == w.from ? 0 : 1;
-  w.pos += w.kb1 - w.kb0;
+  const int rel = (int)(w.pos / c.ends), at = (int)(w.pos - (int64_t)rel * c.ends);
+  const int n = (int)min((int64_t)(c.ends - at), w.to - w.pos);
+  w.tile = p.whole + rel;
+  w.kb0 = p.head + at;
+  w.kb1 = w.kb0 + n;
+  w.slot = pair + rel;  // left + (pair - left) + rel: unique, since both only rise
+  w.pos += n;
   return true;
 }
 // tile number -> plane, row tile, column tile: `group` row tiles at a time,
@@ -156,8 +184,8 @@ __device__ __forceinline__ void store4(float* o, const float (&v)[4]) {
 // A partial tile of TN columns: float4 of 4 columns, [block][row quarter][TN / 4]
 // [row], so that the 32 lanes of a warp store and load 512 bytes in a line.
 template <int TN>
-__device__ __forceinline__ float4* part_at(const P& p, int64_t pair, int slot, int part) {
-  return reinterpret_cast<float4*>(p.part) + ((pair * 2 + slot) * 8 + part) * (TN / 4 * 32);
+__device__ __forceinline__ float4* part_at(const P& p, int64_t slot, int part) {
+  return reinterpret_cast<float4*>(p.part) + (slot * 8 + part) * (TN / 4 * 32);
 }
 
 // Joins the partial tiles: block x handles one cut tile's eighth (block of the
@@ -168,21 +196,20 @@ __global__ void __launch_bounds__(256) glu_join_kernel(const P p, int pairs) {
   const int rel = blockIdx.x >> 3, tile = p.whole + rel;
   int z, mt, nt;
   tile_at(p, tile, z, mt, nt);
-  const int64_t t0 = (int64_t)rel * p.nkb, t1 = t0 + p.nkb;
-  const int64_t left = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
-  int first = (int)(t0 * pairs / (left * p.nkb));
-  while (first > 0 && cut(p, first, pairs) > t0) --first;
-  while (cut(p, first + 1, pairs) <= t0) ++first;
-  if (cut(p, first, pairs) <= t0 && cut(p, first + 1, pairs) >= t1) return;  // done whole
+  const Cut c(p);
+  // the pairs that hold parts of this tile's end
+  const int64_t t0 = (int64_t)rel * c.ends, t1 = t0 + c.ends;
+  int first = (int)(t0 * (pairs - c.left) / ((int64_t)c.left * c.ends));
+  while (first > 0 && c.begin(first, pairs) > t0) --first;
+  while (c.begin(first + 1, pairs) <= t0) ++first;
   const int row0 = mt * 2 * kHalf + (part >> 2) * kHalf + (part & 3) * 32;
   E* out = static_cast<E*>(p.out);
   const bool by_four = p.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(E)) == 0;
   for (int i = threadIdx.x; i < TN / 4 * 32; i += 256) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int pr = first; pr < pairs && cut(p, pr, pairs) < t1; ++pr) {
-      const int64_t a = cut(p, pr, pairs);
-      if (cut(p, pr + 1, pairs) == a) continue;
-      const float4 v = __ldcs(part_at<TN>(p, pr, a >= t0 ? 0 : 1, part) + i);
+    float4 s = __ldcs(part_at<TN>(p, rel, part) + i);
+    for (int j = first; j < pairs - c.left && c.begin(j, pairs) < t1; ++j) {
+      if (c.begin(j + 1, pairs) == c.begin(j, pairs)) continue;
+      const float4 v = __ldcs(part_at<TN>(p, c.left + j + rel, part) + i);
       s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
     }
     const int row = row0 + (i & 31), col = nt * TN + (i >> 5) * 4;
@@ -200,17 +227,20 @@ __global__ void __launch_bounds__(256) glu_join_kernel(const P p, int pairs) {
 // Pairs of blocks at work, and how many tiles (p.whole) they do whole.  Tiles
 // of a last, unfilled round are cut along the contraction, all pairs taking an
 // equal part, where that frees more than `least` blocks of 64 k: what a
-// partial tile costs to write and read again.  With less than half a tile's
-// worth each, the round before is cut too.
+// partial tile costs to write and read again.  A round that is more than four
+// fifths full is left as it is: it would be cut into many small ends.
 inline int plan_pairs(P* p, int num_sms, int least) {
   const int64_t tiles = (int64_t)p->m_tiles * p->n_tiles * p->planes;
   int pairs = std::max(1, std::min(num_sms / 2, kGluMaxPairs));
   p->whole = (int)tiles;
+  p->head = p->nkb;
   const int64_t over = tiles % pairs;
-  if (p->part && over) {
+  if (p->part && over && 5 * over <= 4 * pairs) {
     const int64_t each = (over * p->nkb + pairs - 1) / pairs;
-    if (p->nkb - each > least)
-      p->whole = (int)(tiles - over - (2 * each < p->nkb && tiles > over ? pairs : 0));
+    if (p->nkb - each > least) {
+      p->whole = (int)(tiles - over);
+      p->head = (int)each;
+    }
   }
   if (p->whole == tiles) pairs = (int)std::min<int64_t>(pairs, tiles);
   return pairs;

@@ -24,7 +24,7 @@
 
 #include "common.cuh"
 #include "ops.h"
-#include "tc_common.cuh"
+#include "wait.cuh"
 
 namespace lr {
 namespace {
@@ -556,7 +556,6 @@ __device__ __forceinline__ void push(uint32_t local, uint32_t bar, unsigned rank
 
 typedef std::integral_constant<bool, true> Yes;
 typedef std::integral_constant<bool, false> No;
-constexpr long long kWaitNs = 2000000000LL;
 
 // Where a block works, and which steps of its sequence count, in walk order
 // [va, vb).
@@ -635,7 +634,7 @@ struct Chain {
                                           unsigned rank, unsigned csize, int lane, int* status,
                                           float (&carry)[V], float (&in)[V]) {
     if (csize > 1) {
-      tc::mbar_wait_cluster_bounded(bar, parity, status, kWaitNs);
+      wait_phase<true>(bar, parity, status);
       __syncwarp();
       for (unsigned c = 0; c < csize; ++c) {
         const MapV<V> m = tile_map[c * 32 + lane];
@@ -671,7 +670,7 @@ struct Ring {
     if (cluster_size() > 1) cluster_sync();  // every block runs before it is written to
   }
   __device__ __forceinline__ void wait(int s, int* status) {
-    tc::mbar_wait_bounded(bar0 + 8 * s, (phase >> s) & 1u, status, kWaitNs);
+    wait_phase<false>(bar0 + 8 * s, (phase >> s) & 1u, status);
     phase ^= 1u << s;
   }
 };
