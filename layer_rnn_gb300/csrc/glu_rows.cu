@@ -2,19 +2,24 @@
 //
 // Every weight is used a few times only, so the bytes of W bound the product.
 //
-// bfloat16 rows that 16-byte copies can read: a warp streams tiles of 8
-// features -- their 8 gate rows and 8 up rows of W, 128 bytes (64 k) each --
-// through its own ring of asynchronous copies and multiplies them on the tensor
-// cores (m16n8k16: the 16 rows as M, the tokens as N).  Gate rows take the
-// upper half of a tile and up rows the lower, so that both pre-activations of
-// an output are in one thread.  The order of k inside a product is free: a
-// lane's 16-byte piece is operand as it lies.  The eight warps of a block split
-// K; where x does not fit shared memory the blocks of a cluster split it
-// further.  Sums are joined in a fixed order in float32; one rounding.
+// Rows of 16-byte pieces: a warp multiplies 8 features -- their 8 gate rows and 8
+// up rows of W -- on the tensor cores, the 16 rows as M, the tokens as N.  Gate
+// rows take the upper half of a tile and up rows the lower, so that both
+// pre-activations of an output are in one thread.  The order of k inside a
+// product is free: a lane's 16-byte piece of a row goes from memory into the
+// registers that are the operand, four steps ahead of its use, with no shared
+// memory or barrier between.  (A ring of asynchronous copies took 7.3 us where
+// this takes GLUTOKEN: one token, 1024 x 4096.)
+// bfloat16: m16n8k16.  float32: m16n8k8 in tf32, three products, v = hi + lo with
+// hi the upper 11 bits: 22 bits an operand; the products of 32 k are added to sums
+// in float32, which round to nearest (the tensor core's cut off).
 //
-// Other rows (float32, or a K that is no multiple of 8): fused multiply-adds,
-// a warp taking two features and up to eight tokens at a time, the lanes
-// splitting K.
+// A block holds x in shared memory: two warps side by side along the features,
+// four along K; where x does not fit the blocks of a cluster split K further.
+// Sums are joined in a fixed order in float32; one rounding.
+//
+// Other rows (K no multiple of 8, float32: 4): fused multiply-adds, a warp
+// taking two features and up to eight tokens at a time, the lanes splitting K.
 #include <algorithm>
 
 #include "common.cuh"
@@ -24,17 +29,18 @@
 namespace lr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 4;
-constexpr int kStageBytes = 16 * 128;
-constexpr int kXBytes = 64 * 1024;  // x of one block at most
+constexpr int kAlong = 4, kBeside = 2;        // warps of a block along K, along features
+constexpr int kWarps = kAlong * kBeside, kThreads = 32 * kWarps;
+constexpr int kFeatures = 8 * kBeside;        // of a block
+constexpr int kAhead = 4;                     // steps whose loads are under way
+constexpr int kXBytes = 64 * 1024;            // x of one block at most
 
 struct RowsP {
-  int M, K, F, nkb, tiles, tok, act;
-  const bf16* x;
-  const bf16* W;
-  bf16* y;
-  uint32_t x_bytes;
+  int M, F, pieces, steps, m0, tok, act;      // pieces: 16 bytes of a row; 8 of them a step
+  const uint4* x;
+  const uint4* W;
+  void* y;
+  int x_bytes;
 };
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -44,20 +50,25 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// v = hi + lo, hi its nearest value with 11 significant bits (NaN and infinities
+// stay in hi)
+__device__ __forceinline__ void split(uint32_t v, uint32_t& hi, uint32_t& lo) {
+  hi = (v & 0x7f800000u) == 0x7f800000u ? v : (v + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(__uint_as_float(v) - __uint_as_float(hi));
 }
 __device__ __forceinline__ unsigned cl_size() {
   unsigned n;
@@ -80,52 +91,40 @@ __device__ __forceinline__ void st_rank0(float2* local, float a, float b) {
 }
 
 // NT: token tiles of 8
-template <int NT>
+template <bool F32, int NT>
 __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kCols = 8 * NT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int along = warp % kAlong, beside = warp / kAlong;
   const unsigned csize = cl_size(), rank = cl_rank();
-  const int m0 = blockIdx.y * p.tok, toks = min(p.tok, p.M - m0);
-  const int kb0 = (int)((int64_t)rank * p.nkb / csize), kb1 = (int)((int64_t)(rank + 1) * p.nkb / csize);
-  const int clusters = gridDim.x / csize, first = blockIdx.x / csize;
-  const int per = (kb1 - kb0 + kWarps - 1) / kWarps;
-  const int items = (first < p.tiles ? (p.tiles - 1 - first) / clusters + 1 : 0) * per;
-  unsigned char* ring = smem + p.x_bytes + warp * (kStages * kStageBytes);
-  float* red = reinterpret_cast<float*>(smem + p.x_bytes + kWarps * kStages * kStageBytes);
-  float2* gather = reinterpret_cast<float2*>(red + 2 * kWarps * 16 * kCols);
-  const uint32_t ring_at = smem_at(ring), xs_at = smem_at(smem);
-
-  int it_tile = first, it_kb = 0;
-  // 16-byte piece c of row r at piece c ^ swz(r): eight lanes that read one
-  // piece column of two rows touch all banks
-  auto swz = [](int r) { return ((r & 1) << 2) | ((r >> 1) & 3); };
-  auto issue = [&](int s) {
-    const int kb = kb0 + it_kb * kWarps + warp;
-    if (it_tile < p.tiles && kb < kb1) {
+  const int s0 = (int)((int64_t)rank * p.steps / csize), s1 = (int)((int64_t)(rank + 1) * p.steps / csize);
+  const int first = s0 + along, steps = first < s1 ? (s1 - first + kAlong - 1) / kAlong : 0;
+  const int f0 = (int)(blockIdx.x / csize) * kFeatures, f = min(f0 + beside * 8 + g, p.F - 1);
+  // features past the end read the last one's weights, pieces past a row its last
+  // one (which meets x = 0), tokens past the last one its x: their sums are dropped
+  const uint4* gate = p.W + (int64_t)f * p.pieces;
+  const uint4* up = gate + (int64_t)p.F * p.pieces;
+  uint4 w[kAhead][2][2];
+  auto fetch = [&](int slot, int i) {
+    if (i >= steps) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = j * 4 + (lane >> 3), c = lane & 7;
-        const int f = it_tile * 8 + (row & 7), k = kb * 64 + c * 8;
-        const bool ok = f < p.F && k < p.K;
-        copy16(ring_at + s * kStageBytes + row * 128 + ((c ^ swz(row)) << 4),
-               p.W + (ok ? (int64_t)(row < 8 ? f : p.F + f) * p.K + k : 0), ok);
-      }
+    for (int u = 0; u < 2; ++u) {
+      const int at = min((first + i * kAlong) * 8 + u * 4 + t, p.pieces - 1);
+      w[slot][u][0] = __ldcs(gate + at);
+      w[slot][u][1] = __ldcs(up + at);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++it_kb == per) { it_kb = 0; it_tile += clusters; }
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
+  for (int i = 0; i < kAhead; ++i) fetch(i, i);
 
-  // x: 16-byte piece (block of 64 k, half h, token, t) holds k = 64 kb + 8 (t + 4 h)
-  for (int i = threadIdx.x; i < (kb1 - kb0) * 8 * toks; i += kThreads) {
-    const int c = i & 7, r = i >> 3, kb = r / toks, m = r - kb * toks;
-    const int k = (kb0 + kb) * 64 + c * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (k < p.K) v = __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(m0 + m) * p.K + k));
-    reinterpret_cast<uint4*>(smem)[((kb * 2 + (c >> 2)) * toks + m) * 4 + (c & 3)] = v;
+  // x: piece q of token m at ((q / 4) tokens + m) 4 + q % 4
+  for (int i = threadIdx.x; i < (s1 - s0) * 8 * p.tok; i += kThreads) {
+    const int m = i / ((s1 - s0) * 8), q = i - m * ((s1 - s0) * 8), at = s0 * 8 + q;
+    copy16(smem_at(smem) + (((q >> 2) * p.tok + m) * 4 + (q & 3)) * 16,
+           p.x + (int64_t)(p.m0 + m) * p.pieces + min(at, p.pieces - 1), at < p.pieces);
   }
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
   float acc[NT][4];
@@ -133,87 +132,118 @@ __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-  int tile = first, kbi = 0, par = 0;
-  const uint32_t row_at = ring_at + g * 128;
-  for (int it = 0, s = 0; it < items; ++it, s = s + 1 == kStages ? 0 : s + 1) {
-    issue(s == 0 ? kStages - 1 : s - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    __syncwarp();
-    const int kb = kb0 + kbi * kWarps + warp;
-    if (kb < kb1) {
+  const unsigned char* xa[NT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = row_at + s * kStageBytes + (((t + 4 * h) ^ swz(g)) << 4);
-        const uint4 a = lds128(at), b = lds128(at + 1024);
-        const uint32_t xa = xs_at + (uint32_t)((((kb - kb0) * 2 + h) * toks + g) * 4 + t) * 16;
+  for (int nt = 0; nt < NT; ++nt)
+    xa[nt] = smem + (along * 2 * p.tok + min(nt * 8 + g, p.tok - 1)) * 64 + t * 16;
+  const int x_quad = p.tok * 64, x_step = kAlong * 2 * x_quad;
+  for (int i0 = 0; i0 < steps; i0 += kAhead) {
+#pragma unroll
+    for (int slot = 0; slot < kAhead; ++slot) {
+      if (i0 + slot >= steps) break;
+      float big[F32 ? NT : 1][4], rest[F32 ? NT : 1][4];
+      if (F32)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) big[F32 ? nt : 0][i] = rest[F32 ? nt : 0][i] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 a = w[slot][u][0], b = w[slot][u][1];
+        uint32_t ah[4], al[4], bh[4], bl[4];
+        if (F32) {
+          split(a.x, ah[0], al[0]); split(a.y, ah[1], al[1]);
+          split(a.z, ah[2], al[2]); split(a.w, ah[3], al[3]);
+          split(b.x, bh[0], bl[0]); split(b.y, bh[1], bl[1]);
+          split(b.z, bh[2], bl[2]); split(b.w, bh[3], bl[3]);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (nt * 8 + g < toks) v = lds128(xa + nt * 512);
-          mma(acc[nt], a.x, b.x, a.y, b.y, v.x, v.y);
-          mma(acc[nt], a.z, b.z, a.w, b.w, v.z, v.w);
-        }
-      }
-    }
-    __syncwarp();
-    if (++kbi < per) continue;
-    kbi = 0;
-    float* rw = red + par * (kWarps * 16 * kCols);
+          const uint4 v = *reinterpret_cast<const uint4*>(xa[nt] + u * x_quad);
+          if (F32) {
+            uint32_t xh[4], xl[4];
+            split(v.x, xh[0], xl[0]); split(v.y, xh[1], xl[1]);
+            split(v.z, xh[2], xl[2]); split(v.w, xh[3], xl[3]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* d = rw + (warp * 16 + g) * kCols + nt * 8 + 2 * t;
-      *reinterpret_cast<float2*>(d) = make_float2(acc[nt][0], acc[nt][1]);
-      *reinterpret_cast<float2*>(d + 8 * kCols) = make_float2(acc[nt][2], acc[nt][3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-    }
-    __syncthreads();
-    const int f0 = tile * 8;
-    for (int i = threadIdx.x; i < 8 * toks; i += kThreads) {
-      const int r = i & 7, m = i >> 3;
-      float gv = 0.f, uv = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        gv += rw[(w * 16 + r) * kCols + m];
-        uv += rw[(w * 16 + 8 + r) * kCols + m];
-      }
-      if (csize > 1)
-        st_rank0(gather + (par * csize + rank) * (8 * kCols) + i, gv, uv);
-      else if (f0 + r < p.F)
-        p.y[(int64_t)(m0 + m) * p.F + f0 + r] = __float2bfloat16_rn(glu::value(gv, p.act) * uv);
-    }
-    if (csize > 1) {
-      cl_sync();
-      if (rank == 0)
-        for (int i = threadIdx.x; i < 8 * toks; i += kThreads) {
-          const int r = i & 7, m = i >> 3;
-          float gv = 0.f, uv = 0.f;
-          for (unsigned c = 0; c < csize; ++c) {
-            const float2 v = gather[(par * csize + c) * (8 * kCols) + i];
-            gv += v.x;
-            uv += v.y;
+            for (int h = 0; h < 4; h += 2) {
+              float(&m)[4] = big[F32 ? nt : 0], (&r)[4] = rest[F32 ? nt : 0];
+              mma_tf32(m, ah[h], bh[h], ah[h + 1], bh[h + 1], xh[h], xh[h + 1]);
+              mma_tf32(r, ah[h], bh[h], ah[h + 1], bh[h + 1], xl[h], xl[h + 1]);
+              mma_tf32(r, al[h], bl[h], al[h + 1], bl[h + 1], xh[h], xh[h + 1]);
+            }
+          } else {
+            mma_bf16(acc[nt], a.x, b.x, a.y, b.y, v.x, v.y);
+            mma_bf16(acc[nt], a.z, b.z, a.w, b.w, v.z, v.w);
           }
-          if (f0 + r < p.F)
-            p.y[(int64_t)(m0 + m) * p.F + f0 + r] = __float2bfloat16_rn(glu::value(gv, p.act) * uv);
         }
+      }
+      if (F32)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[nt][i] += big[F32 ? nt : 0][i] + rest[F32 ? nt : 0][i];
+      fetch(slot, i0 + slot + kAhead);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) xa[nt] += x_step;
     }
-    par ^= 1;
-    tile += clusters;
+  }
+
+  // (gate, up) sums: [warp along K][token][feature]
+  float2* red = reinterpret_cast<float2*>(smem + p.x_bytes);
+  float2* across = red + kAlong * kCols * kFeatures;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      red[(along * kCols + nt * 8 + 2 * t + u) * kFeatures + beside * 8 + g] =
+          make_float2(acc[nt][u], acc[nt][2 + u]);
+  __syncthreads();
+  auto put = [&](int i, float gv, float uv) {
+    const int fi = f0 + i % kFeatures;
+    if (fi >= p.F) return;
+    const int64_t at = (int64_t)(p.m0 + i / kFeatures) * p.F + fi;
+    const float v = glu::value(gv, p.act) * uv;
+    if (F32) static_cast<float*>(p.y)[at] = v;
+    else static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
+  };
+  const int part = p.tok * kFeatures;
+  for (int i = threadIdx.x; i < part; i += kThreads) {
+    float gv = 0.f, uv = 0.f;
+#pragma unroll
+    for (int k = 0; k < kAlong; ++k) {
+      const float2 v = red[k * kCols * kFeatures + i];
+      gv += v.x;
+      uv += v.y;
+    }
+    if (csize > 1) st_rank0(across + (int)rank * part + i, gv, uv);
+    else put(i, gv, uv);
+  }
+  if (csize > 1) {
+    __syncwarp();
+    cl_sync();
+    if (rank == 0)
+      for (int i = threadIdx.x; i < part; i += kThreads) {
+        float gv = 0.f, uv = 0.f;
+        for (unsigned c = 0; c < csize; ++c) {
+          const float2 v = across[c * part + i];
+          gv += v.x;
+          uv += v.y;
+        }
+        put(i, gv, uv);
+      }
   }
 }
 
-template <int NT>
-cudaError_t launch_rows(RowsP p, int csize, int num_sms, cudaStream_t st) {
-  auto kernel = glu_rows_kernel<NT>;
-  p.x_bytes = (uint32_t)((p.nkb + csize - 1) / csize * 128 * p.tok);
-  const size_t smem = p.x_bytes + kWarps * kStages * kStageBytes + 2 * kWarps * 16 * 8 * NT * 4 +
-                      (csize > 1 ? 2 * csize * 8 * 8 * NT * 8 : 0);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+template <bool F32, int NT>
+cudaError_t launch_rows(RowsP p, int csize, cudaStream_t st) {
+  auto kernel = glu_rows_kernel<F32, NT>;
+  p.x_bytes = (p.steps + csize - 1) / csize * 128 * p.tok;
+  const size_t smem = (size_t)p.x_bytes + kAlong * 8 * NT * kFeatures * 8 +
+                      (csize > 1 ? (size_t)csize * p.tok * kFeatures * 8 : 0);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
   if (e != cudaSuccess) return e;
-  const int per_sm = std::max(1, std::min(3, (int)(224 * 1024 / (smem + 1024))));
-  const int clusters = std::min(p.tiles, std::max(1, num_sms * per_sm / csize));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * csize), (unsigned)((p.M + p.tok - 1) / p.tok));
+  cfg.gridDim = dim3((unsigned)((p.F + kFeatures - 1) / kFeatures * csize));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -226,6 +256,35 @@ cudaError_t launch_rows(RowsP p, int csize, int num_sms, cudaStream_t st) {
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return e;
+}
+
+// tokens in passes of 32 at most, fewer where x would not fit eight blocks
+template <bool F32>
+cudaError_t run_rows(const GluArgs& a, cudaStream_t st) {
+  RowsP p = {};
+  const int per = F32 ? 4 : 8;
+  p.M = (int)a.M; p.F = (int)a.F;
+  p.pieces = (int)(a.K / per);
+  p.steps = (p.pieces + 7) / 8;
+  p.act = a.act;
+  p.x = static_cast<const uint4*>(a.x);
+  p.W = static_cast<const uint4*>(a.W);
+  p.y = a.y;
+  auto x_bytes = [&](int c, int tok) { return (int64_t)((p.steps + c - 1) / c) * 128 * tok; };
+  int tok = 32;
+  while (tok > 1 && x_bytes(8, tok) > kXBytes) tok /= 2;
+  for (int64_t m0 = 0; m0 < a.M; m0 += tok) {
+    p.m0 = (int)m0;
+    p.tok = (int)std::min<int64_t>(tok, a.M - m0);
+    int c = 1;
+    while (c < 8 && x_bytes(c, p.tok) > kXBytes) c *= 2;
+    const cudaError_t e = p.tok <= 8    ? launch_rows<F32, 1>(p, c, st)
+                          : p.tok <= 16 ? launch_rows<F32, 2>(p, c, st)
+                          : p.tok <= 24 ? launch_rows<F32, 3>(p, c, st)
+                                        : launch_rows<F32, 4>(p, c, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------
@@ -319,26 +378,13 @@ cudaError_t launch_fma(const GluArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t glu_rows_forward(const GluArgs& a, cudaStream_t st) {
-  if (!a.bf16) return a.K % 4 == 0 ? launch_fma<float, 4>(a, st) : launch_fma<float, 1>(a, st);
-  // at K beyond 8 blocks' shared memory for one token a row is split no further
-  if (a.K % 8 != 0 || a.K > 8 * kXBytes / 2) return launch_fma<bf16, 1>(a, st);
-  RowsP p = {};
-  p.M = (int)a.M; p.K = (int)a.K; p.F = (int)a.F;
-  p.nkb = (int)((a.K + 63) / 64);
-  p.tiles = (int)((a.F + 7) / 8);
-  p.act = a.act;
-  p.x = static_cast<const bf16*>(a.x);
-  p.W = static_cast<const bf16*>(a.W);
-  p.y = static_cast<bf16*>(a.y);
-  auto x_bytes = [&](int c, int tok) { return (int64_t)((p.nkb + c - 1) / c) * 128 * tok; };
-  p.tok = 32;
-  while (p.tok > 1 && (p.tok >= 2 * a.M || x_bytes(8, p.tok) > kXBytes)) p.tok /= 2;
-  p.tok = (int)std::min<int64_t>(p.tok, a.M);
-  int c = 1;
-  while (c < 8 && x_bytes(c, p.tok) > kXBytes) c *= 2;
-  if (p.tok <= 8) return launch_rows<1>(p, c, a.num_sms, st);
-  if (p.tok <= 16) return launch_rows<2>(p, c, a.num_sms, st);
-  return launch_rows<4>(p, c, a.num_sms, st);
+  // beyond eight blocks' shared memory for one token x is split no further
+  const int64_t most = 8 * (int64_t)kXBytes;
+  if (!a.bf16)
+    return a.K % 4 != 0    ? launch_fma<float, 1>(a, st)
+           : a.K * 4 > most ? launch_fma<float, 4>(a, st)
+                            : run_rows<true>(a, st);
+  return a.K % 8 != 0 || a.K * 2 > most ? launch_fma<bf16, 1>(a, st) : run_rows<false>(a, st);
 }
 
 }  // namespace lr
