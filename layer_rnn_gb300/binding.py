@@ -393,6 +393,8 @@ class Ops:
         self.dtype = dtype
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._device = torch._C._cuda_getDevice if self._raw_stream is not None else None
+        self._lib = lib()
         self.h = None
         h = _vp()
         _call("rnn_ops_create", ctypes.byref(h), DTYPES[dtype], flags)
@@ -415,14 +417,14 @@ class Ops:
         # the address of the current stream without a Stream object around it:
         # 3 us less in a call of 10
         if self._raw_stream is not None:
-            return self._raw_stream(self.torch.cuda.current_device())
+            return self._raw_stream(self._device())
         return self.torch.cuda.current_stream().cuda_stream
 
     def _check(self, name, t, shape, dtype=None):
         """A dense tensor of this shape (or None): its address."""
         if t is None:
             return None
-        if t.shape != shape or t.dtype != (dtype or self.tdtype):
+        if t.shape != shape or t.dtype is not (dtype or self.tdtype):
             raise ValueError("%s: expected %s %s, got %s %s" % (
                 name, tuple(shape), dtype or self.tdtype, tuple(t.shape), t.dtype))
         if not t.is_cuda or not t.is_contiguous():

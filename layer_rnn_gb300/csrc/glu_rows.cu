@@ -240,7 +240,9 @@ cudaError_t launch_rows(RowsP p, int csize, cudaStream_t st) {
   p.x_bytes = (p.steps + csize - 1) / csize * 128 * p.tok;
   const size_t smem = (size_t)p.x_bytes + kAlong * 8 * NT * kFeatures * 8 +
                       (csize > 1 ? (size_t)csize * p.tok * kFeatures * 8 : 0);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((p.F + kFeatures - 1) / kFeatures * csize));
@@ -252,7 +254,7 @@ cudaError_t launch_rows(RowsP p, int csize, cudaStream_t st) {
   at[0].val.clusterDim.x = (unsigned)csize;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = csize > 1 ? 1 : 0;  // a launch with the attribute takes 2 us longer
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return e;

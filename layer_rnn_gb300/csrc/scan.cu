@@ -123,94 +123,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st_peer2(float2* local, unsigned rank, float a, float b) {
-  unsigned addr;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-               : "=r"(addr)
-               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(local))), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
-}
-
-// Where a thread works: CV lanes along the channels (V each), kThreads / CV
-// slots along time, L steps a slot.
-template <int V, int CV, int L>
-struct Shape {
-  static constexpr int kSlots = kThreads / CV;
-  static constexpr int kChannels = CV * V;
-  static constexpr int kTile = kSlots * L;
-  static constexpr int kParts = kThreads / kChannels;  // threads a channel when slots are joined
-  static constexpr int kPer = kSlots / kParts;         // slots each of them joins
-  static_assert(kParts >= 1 && kPer >= 1 && kParts * kPer == kSlots, "shape");
-};
-
-// The tile's maps, slot by slot, and what goes into each slot.  Walks of the
-// two passes differ in direction only: slot order s is the order in which the
-// state passes through them.
-template <int V, int CV, int L>
-struct Join {
-  using S = Shape<V, CV, L>;
-  float2 slot[S::kSlots][S::kChannels];   // (A, B) of each slot; then .x = value going in
-  float2 part[S::kParts][S::kChannels];
-  float2 tile[2][8][S::kChannels];        // the cluster's tiles (by parity of the round)
-
-  // state into the slots, given each slot's map in `slot`: returns the value
-  // that leaves the whole round (all tiles of the cluster); `carry` enters
-  // it.  Channel and part of this thread: tid % kChannels, tid / kChannels;
-  // only these threads' carry matters.  All threads of the cluster call it.
-  __device__ __forceinline__ float run(float carry, int round, unsigned rank, unsigned csize) {
-    const int c = threadIdx.x % S::kChannels, q = threadIdx.x / S::kChannels;
-    __syncthreads();
-    float A = 1.f, B = 0.f;
-#pragma unroll
-    for (int k = 0; k < S::kPer; ++k) {
-      const float2 m = slot[q * S::kPer + k][c];
-      B = fmaf(m.x, B, m.y);
-      A *= m.x;
-    }
-    if (S::kParts > 1) {
-      part[q][c] = make_float2(A, B);
-      __syncthreads();
-    }
-    float tA = 1.f, tB = 0.f, pA = 1.f, pB = 0.f;  // whole tile; the parts before this one
-    if (S::kParts > 1) {
-#pragma unroll
-      for (int k = 0; k < S::kParts; ++k) {
-        if (k == q) { pA = tA; pB = tB; }
-        const float2 m = part[k][c];
-        tB = fmaf(m.x, tB, m.y);
-        tA *= m.x;
-      }
-    } else {
-      tA = A; tB = B;
-    }
-    float in = carry, out = 0.f;
-    if (csize > 1) {
-      for (unsigned r = q; r < csize; r += S::kParts)
-        st_peer2(&tile[round & 1][rank][c], r, tA, tB);
-      cluster_sync();
-      float h = carry;
-      for (unsigned r = 0; r < csize; ++r) {
-        if (r == rank) in = h;
-        const float2 m = tile[round & 1][r][c];
-        h = fmaf(m.x, h, m.y);
-      }
-      out = h;
-    } else {
-      out = fmaf(tA, carry, tB);
-    }
-    float h = fmaf(pA, in, pB);
-#pragma unroll
-    for (int k = 0; k < S::kPer; ++k) {
-      float2& m = slot[q * S::kPer + k][c];
-      const float nh = fmaf(m.x, h, m.y);
-      m.x = h;
-      h = nh;
-    }
-    __syncthreads();
-    return out;
-  }
-};
-
 // channel vector of a lane
 struct Lane {
   bool live;
@@ -236,244 +148,14 @@ __device__ __forceinline__ Lane lane_of(const ScanP& p, int64_t vec, int V, int 
   return l;
 }
 
-template <typename E, int V, int CV, int L, bool GATE>
-__global__ void __launch_bounds__(kThreads) scan_forward_kernel(const ScanP p) {
-  using S = Shape<V, CV, L>;
-  constexpr int G = GATE ? 3 : 2;
-  __shared__ Join<V, CV, L> join;
-  const unsigned csize = cluster_size(), rank = cluster_rank();
-  const int cv = threadIdx.x % CV, slot = threadIdx.x / CV;
-  const int64_t group = blockIdx.x / csize;
-  const Lane l = lane_of(p, group * CV + cv, V, G);
-  const E* gx = static_cast<const E*>(p.gx) + l.g0;
-  E* y = static_cast<E*>(p.y) + l.y0;
-  const int64_t tg = p.N * p.ldg, ty = p.N * p.ldy;
-  // the carried state of channel threadIdx.x % kChannels
-  float carry = 0.f;
-  {
-    const int c = threadIdx.x % S::kChannels;
-    const Lane k = lane_of(p, group * CV + c / V, V, G);
-    if (k.live && p.h0) carry = p.h0[k.state + c % V];
-  }
-  const int64_t rounds = (p.T + S::kTile * csize - 1) / (S::kTile * csize);
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t w0 = (r * csize + rank) * S::kTile + slot * L;  // first step of the walk
-    Raw<E, V> rp[L], rz[L];
-    unsigned valid = 0;
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      const int64_t t = l.d ? p.T - 1 - (w0 + k) : w0 + k;
-      if (l.live && w0 + k < p.T && t < l.len) {
-        valid |= 1u << k;
-        rp[k] = load_raw<E, V>(gx + t * tg);
-        rz[k] = load_raw<E, V>(gx + t * tg + p.H);
-      }
-    }
-    float a[L][V], b[L][V], A[V], B[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      float pv[V], zv[V];
-      unpack(rp[k], pv);
-      unpack(rz[k], zv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float f, i;
-        gate_pair(pv[v], f, i);
-        const bool ok = (valid >> k) & 1u;
-        a[k][v] = ok ? f : 1.f;
-        b[k][v] = ok ? i * zv[v] : 0.f;
-        B[v] = fmaf(a[k][v], B[v], b[k][v]);
-        A[v] *= a[k][v];
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) join.slot[slot][cv * V + v] = make_float2(A[v], B[v]);
-    carry = join.run(carry, (int)(r & 1), rank, csize);
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = join.slot[slot][cv * V + v].x;
-    if (p.states && l.live && w0 < p.T && w0 % kScanState == 0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) p.states[w0 / kScanState * p.states_row + l.gh + v] = h[v];
-    }
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      const int64_t t = l.d ? p.T - 1 - (w0 + k) : w0 + k;
-      const bool ok = (valid >> k) & 1u;
-      float out[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = fmaf(a[k][v], h[v], b[k][v]);
-        out[v] = ok ? h[v] : 0.f;
-      }
-      if (GATE && ok) {
-        float q[V];
-        unpack(load_raw<E, V>(gx + t * tg + 2 * p.H), q);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float o, i;
-          gate_pair(q[v], o, i);
-          out[v] *= o;
-        }
-      }
-      if (l.live && w0 + k < p.T) store_v(y + t * ty, out);
-    }
-  }
-  if (p.hy && rank == 0) {
-    const int c = threadIdx.x % S::kChannels;
-    const Lane k = lane_of(p, group * CV + c / V, V, G);
-    if (threadIdx.x < S::kChannels && k.live) p.hy[k.state + c % V] = carry;
-  }
-}
-
-template <typename E, int V, int CV, int L, bool GATE>
-__global__ void __launch_bounds__(kThreads) scan_backward_kernel(const ScanP p) {
-  using S = Shape<V, CV, L>;
-  constexpr int G = GATE ? 3 : 2;
-  static_assert(S::kTile % kScanState == 0, "a tile starts at a saved state");
-  __shared__ Join<V, CV, L> join;
-  const unsigned csize = cluster_size(), rank = cluster_rank();
-  const int cv = threadIdx.x % CV, slot = threadIdx.x / CV;
-  const int64_t group = blockIdx.x / csize;
-  const Lane l = lane_of(p, group * CV + cv, V, G);
-  const E* gx = static_cast<const E*>(p.gx) + l.g0;
-  E* dgx = static_cast<E*>(p.dgx) + l.g0;
-  const E* dy = static_cast<const E*>(p.dy) + l.y0;
-  const int64_t tg = p.N * p.ldg, ty = p.N * p.ldy;
-  const int c = threadIdx.x % S::kChannels;
-  const Lane kc = lane_of(p, group * CV + c / V, V, G);
-  float carry = 0.f;
-  if (kc.live && p.dhy) carry = p.dhy[kc.state + c % V];
-  const int64_t tiles = (p.T + S::kTile - 1) / S::kTile;
-  const int64_t rounds = (tiles + csize - 1) / csize;
-  for (int64_t r = 0; r < rounds; ++r) {
-    // tiles from the end of the walk; a tile before the start is empty
-    const int64_t tile = tiles - 1 - (r * csize + rank);
-    const int64_t w0 = tile * S::kTile + slot * L;
-    Raw<E, V> rp[L], rz[L], rd[L], rq[GATE ? L : 1];
-    unsigned valid = 0;
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      const int64_t t = l.d ? p.T - 1 - (w0 + k) : w0 + k;
-      if (l.live && tile >= 0 && w0 + k < p.T && t < l.len) {
-        valid |= 1u << k;
-        rp[k] = load_raw<E, V>(gx + t * tg);
-        rz[k] = load_raw<E, V>(gx + t * tg + p.H);
-        if (GATE) rq[k] = load_raw<E, V>(gx + t * tg + 2 * p.H);
-        rd[k] = load_raw<E, V>(dy + t * ty);
-      }
-    }
-    float start = 0.f;  // the state at the tile's start, of channel c
-    if (tile >= 0 && kc.live)
-      start = p.states[tile * (S::kTile / kScanState) * p.states_row + kc.gh + c % V];
-    // forward over the tile: the state into each slot
-    float f[L][V], A[V], B[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      float pv[V], zv[V];
-      unpack(rp[k], pv);
-      unpack(rz[k], zv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float i;
-        gate_pair(pv[v], f[k][v], i);
-        const bool ok = (valid >> k) & 1u;
-        f[k][v] = ok ? f[k][v] : 1.f;
-        B[v] = ok ? fmaf(f[k][v], B[v], i * zv[v]) : B[v];
-        A[v] *= f[k][v];
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) join.slot[slot][cv * V + v] = make_float2(A[v], B[v]);
-    join.run(start, 0, 0, 1);
-    float h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = join.slot[slot][cv * V + v].x;
-    // against the walk: slot s of this order is the tile's slot kSlots - 1 - s
-#pragma unroll
-    for (int v = 0; v < V; ++v) B[v] = 0.f;
-#pragma unroll
-    for (int k = L - 1; k >= 0; --k) {
-      float dv[V], o[V];
-      unpack(rd[k], dv);
-      if (GATE) unpack(rq[GATE ? k : 0], o);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const bool ok = (valid >> k) & 1u;
-        float i;
-        if (GATE) gate_pair(o[v], o[v], i); else o[v] = 1.f;
-        B[v] = ok ? f[k][v] * fmaf(dv[v], o[v], B[v]) : B[v];
-      }
-    }
-    __syncthreads();  // the states going in have been read
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      join.slot[S::kSlots - 1 - slot][cv * V + v] = make_float2(A[v], B[v]);
-    carry = join.run(carry, (int)(r & 1), rank, csize);
-    float e[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = join.slot[S::kSlots - 1 - slot][cv * V + v].x;
-    // h before each step, then the gradients against the walk
-    float hb[L][V];
-#pragma unroll
-    for (int k = 0; k < L; ++k) {
-      float zv[V];
-      unpack(rz[k], zv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        hb[k][v] = h[v];
-        const bool ok = (valid >> k) & 1u;
-        // (1 - f) z + f h as z + f (h - z) would lose small differences; the
-        // form of the forward pass is kept
-        float fv, i, pv[V];
-        unpack(rp[k], pv);
-        gate_pair(pv[v], fv, i);
-        h[v] = ok ? fmaf(fv, h[v], i * zv[v]) : h[v];
-      }
-    }
-#pragma unroll
-    for (int k = L - 1; k >= 0; --k) {
-      const int64_t t = l.d ? p.T - 1 - (w0 + k) : w0 + k;
-      const bool ok = (valid >> k) & 1u;
-      float pv[V], zv[V], dv[V], qv[V], gp[V], gz[V], gq[V];
-      unpack(rp[k], pv);
-      unpack(rz[k], zv);
-      unpack(rd[k], dv);
-      if (GATE) unpack(rq[GATE ? k : 0], qv);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float fv, i, o = 1.f, oi = 0.f;
-        gate_pair(pv[v], fv, i);
-        if (GATE) gate_pair(qv[v], o, oi);
-        const float hn = fmaf(fv, hb[k][v], i * zv[v]);
-        const float dh = fmaf(dv[v], o, e[v]);
-        gz[v] = ok ? dh * i : 0.f;
-        gp[v] = ok ? dh * (hb[k][v] - zv[v]) * (fv * i) : 0.f;
-        gq[v] = ok ? dv[v] * hn * (o * oi) : 0.f;
-        e[v] = ok ? fv * dh : e[v];
-      }
-      if (l.live && tile >= 0 && w0 + k < p.T) {
-        store_v(dgx + t * tg, gp);
-        store_v(dgx + t * tg + p.H, gz);
-        if (GATE) store_v(dgx + t * tg + 2 * p.H, gq);
-      }
-    }
-    __syncthreads();  // the slots have been read
-  }
-  if (p.dh0 && rank == 0 && threadIdx.x < S::kChannels && kc.live)
-    p.dh0[kc.state + c % V] = carry;
-}
-
 // ---------------------------------------------------------------------------
-// Rows that TMA can read: a block takes 128 bytes of a row (64 bf16 or 32
+// A block takes 128 bytes of a row (64 bf16 or 32
 // float32 channels of one sequence and direction), each of its four warps 16
 // consecutive steps, a lane a 4-byte word.  Tiles of 64 steps arrive in a ring
 // of shared memory, so that the loads of the next tiles run under the
-// arithmetic of this one; every input is still read once from memory.
+// arithmetic of this one; every input is still read once from memory.  Rows that
+// TMA cannot read (not on 16 bytes: odd widths and pitches) are loaded by the lanes
+// themselves where they are used, two at a time where a pair starts on a word.
 //
 // The arithmetic comes close to the memory's time (25 instructions an element
 // forward, 50 backward), hence four warps with 16 steps each rather than eight
@@ -481,12 +163,14 @@ __global__ void __launch_bounds__(kThreads) scan_backward_kernel(const ScanP p) 
 // exchange their tiles' maps by asynchronous stores that count on a barrier of
 // the receiver; a cluster-wide barrier instead cost 5 us a round.
 // ---------------------------------------------------------------------------
-constexpr int kWarps = 4, kSteps = 16, kTileSteps = kWarps * kSteps;
-constexpr int kRow = 128, kPlane = kTileSteps * kRow;
+constexpr int kWarps = 4, kSteps = 16;  // of a block; of a warp
+constexpr int kTileSteps = kWarps * kSteps, kRow = 128, kPlane = kTileSteps * kRow;
 static_assert(kTileSteps == kScanState, "a tile starts at a saved state");
 
 struct TileP {
   CUtensorMap gx, dy;
+  const void* gx_at;
+  const void* dy_at;
   int T, N, H, D, groups_h;  // groups_h: channel groups of a direction
   int64_t ldg, ldy;
   const int* lengths;
@@ -531,6 +215,31 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
+// a lane's word from memory and to it; n: how many of its channels exist
+__device__ __forceinline__ uint32_t get_word(const float* p, int n) {
+  return n > 0 ? __float_as_uint(__ldg(p)) : 0u;
+}
+__device__ __forceinline__ uint32_t get_word(const bf16* p, int n) {
+  const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+  if (n == 2 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) return __ldg(reinterpret_cast<const unsigned*>(p));
+  uint32_t w = 0;
+  if (n > 0) w = __ldg(h);
+  if (n > 1) w |= (uint32_t)__ldg(h + 1) << 16;
+  return w;
+}
+__device__ __forceinline__ void put_word(float* p, uint32_t w, int n) {
+  if (n > 0) *p = __uint_as_float(w);
+}
+__device__ __forceinline__ void put_word(bf16* p, uint32_t w, int n) {
+  unsigned short* h = reinterpret_cast<unsigned short*>(p);
+  if (n == 2 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) {
+    *reinterpret_cast<uint32_t*>(p) = w;
+    return;
+  }
+  if (n > 0) h[0] = (unsigned short)w;
+  if (n > 1) h[1] = (unsigned short)(w >> 16);
+}
+
 // maps of V channels, one lane: (A, B) pairs
 template <int V> struct alignas(8 * V) MapV { float2 m[V]; };
 
@@ -563,7 +272,7 @@ template <typename E>
 struct Place {
   static constexpr int V = Word<E>::V, kCh = 32 * V;
   int n, d, j0, j, va, vb;
-  bool live;
+  int live;  // channels of this lane that exist
   int64_t state, gh;
   __device__ __forceinline__ Place(const TileP& p, int group) {
     const int lane = threadIdx.x & 31;
@@ -572,7 +281,7 @@ struct Place {
     d = nd - n * p.D;
     j0 = (group - nd * p.groups_h) * kCh;
     j = j0 + lane * V;
-    live = j < p.H;
+    live = min(max(p.H - j, 0), V);
     state = ((int64_t)d * p.N + n) * p.H + j;
     gh = (int64_t)nd * p.H + j;
     const int len = p.lengths ? min(max(p.lengths[n], 0), p.T) : p.T;
@@ -675,11 +384,11 @@ struct Ring {
   }
 };
 
-template <typename E, bool GATE, int ST>
+template <typename E, bool GATE, bool TMA, int ST>
 __global__ void __launch_bounds__(32 * kWarps, 3)
     scan_forward_tiles(const __grid_constant__ TileP p) {
   constexpr int G = GATE ? 3 : 2, V = Word<E>::V, L = kSteps;
-  constexpr int kStage = G * kPlane;
+  constexpr int kStage = TMA ? G * kPlane : 0;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[ST + 2];
   __shared__ __align__(16) MapV<V> map[2][kWarps][32];
@@ -702,12 +411,12 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     for (int b = 0; b < G; ++b)
       tile_load(ring.base + s * kStage + b * kPlane, &p.gx, (at.d * G + b) * p.H + at.j0, at.n, t0, bar);
   };
-  if (threadIdx.x == 0)
+  if (TMA && threadIdx.x == 0)
     for (int r = 0; r < ST; ++r) load(r, r);
   const Words words(warp, at.d);
   float carry[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = at.live && p.h0 ? p.h0[at.state + v] : 0.f;
+  for (int v = 0; v < V; ++v) carry[v] = v < at.live && p.h0 ? p.h0[at.state + v] : 0.f;
   const int64_t ty = (int64_t)p.N * p.ldy * (int64_t)sizeof(E);
   const int64_t step = at.d ? -ty : ty;
   char* y0 = static_cast<char*>(p.y) +
@@ -719,8 +428,29 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     const int64_t w0 = first_of(r), ws = w0 + warp * L;
     const bool on = ws < at.vb && ws + L > at.va;     // this warp has steps that count
     const bool all = ws >= at.va && ws + L <= at.vb;  // and no others
-    if (active(w0)) ring.wait(s, p.status);
+    if (TMA && active(w0)) ring.wait(s, p.status);
     const uint32_t stage = ring.base + s * kStage;
+    // a step's word of plane b (gx: blocks of H; then dy)
+    auto word = [&](int b, int k) -> uint32_t {
+      if constexpr (TMA) {
+        return words.get(stage + b * kPlane, k);
+      } else {
+        const int64_t w = ws + k, t = at.d ? p.T - 1 - w : w;
+        if (!(w >= at.va && w < at.vb)) return 0u;
+        if (b < G)
+          return get_word(static_cast<const E*>(p.gx_at) + (t * p.N + at.n) * p.ldg +
+                              (int64_t)(at.d * G + b) * p.H + at.j, at.live);
+        return get_word(static_cast<const E*>(p.dy_at) + (t * p.N + at.n) * p.ldy +
+                            (int64_t)at.d * p.H + at.j, at.live);
+      }
+    };
+    auto put = [&](char* row, uint32_t w) {
+      if constexpr (TMA) {
+        if (at.live) __stcs(reinterpret_cast<uint32_t*>(row) + lane, w);
+      } else {
+        put_word(reinterpret_cast<E*>(row) + lane * V, w, at.live);
+      }
+    };
     float a[L][V], b[L][V], A[V], B[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
@@ -728,8 +458,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
       for (int k = 0; k < L; ++k) {
         float pv[V], zv[V];
-        Word<E>::get(words.get(stage, k), pv);
-        Word<E>::get(words.get(stage + kPlane, k), zv);
+        Word<E>::get(word(0, k), pv);
+        Word<E>::get(word(1, k), zv);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float i;
@@ -760,7 +490,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     for (int v = 0; v < V; ++v) map[par][warp][lane].m[v] = make_float2(A[v], B[v]);
     __syncthreads();
     // the tile before this one has been used by every warp
-    if (threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
+    if (TMA && threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
     Chain<V, 1> chain;
     chain.join(map[par], warp, lane);
     MapV<V>* tm = tile_map + par * csize * 32;
@@ -771,7 +501,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
       for (int k = 0; k < L; ++k) {
         float q[V];
-        Word<E>::get(words.get(stage + 2 * kPlane, k), q);
+        Word<E>::get(word(2, k), q);
 #pragma unroll
         for (int v = 0; v < V; ++v) o[GATE ? k : 0][v] = gate_one(q[v]);
       }
@@ -781,10 +511,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     before = s;
     if (++s == ST) s = 0;
     if (ws >= p.T) continue;
-    if (p.states && warp == 0 && at.live) {
+    if (p.states && ws % kScanState == 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        p.states[ws / kScanState * ((int64_t)p.N * p.D * p.H) + at.gh + v] = h[v];
+        if (v < at.live) p.states[ws / kScanState * ((int64_t)p.N * p.D * p.H) + at.gh + v] = h[v];
     }
     char* y = y0 + (at.d ? p.T - 1 - ws : ws) * ty;
     if (on && all) {
@@ -796,7 +526,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
           h[v] = fmaf(a[k][v], h[v], b[k][v]);
           out[v] = GATE ? h[v] * o[GATE ? k : 0][v] : h[v];
         }
-        if (at.live) __stcs(reinterpret_cast<uint32_t*>(y) + lane, Word<E>::put(out));
+        put(y, Word<E>::put(out));
       }
     } else {
 #pragma unroll
@@ -812,22 +542,23 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
             out[v] = GATE ? h[v] * o[GATE ? k : 0][v] : h[v];
           }
         }
-        if (at.live && ws + k < p.T) __stcs(reinterpret_cast<uint32_t*>(y) + lane, ok ? Word<E>::put(out) : 0u);
+        if (ws + k < p.T) put(y, ok ? Word<E>::put(out) : 0u);
       }
     }
   }
-  if (p.hy && rank == 0 && warp == 0 && at.live) {
+  if (p.hy && rank == 0 && warp == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.hy[at.state + v] = carry[v];
+    for (int v = 0; v < V; ++v)
+      if (v < at.live) p.hy[at.state + v] = carry[v];
   }
   if (csize > 1) cluster_sync();  // no block leaves before the others' stores to it
 }
 
-template <typename E, bool GATE, int ST>
+template <typename E, bool GATE, bool TMA, int ST>
 __global__ void __launch_bounds__(32 * kWarps, 3)
     scan_backward_tiles(const __grid_constant__ TileP p) {
   constexpr int G = GATE ? 3 : 2, V = Word<E>::V, L = kSteps;
-  constexpr int kStage = (G + 1) * kPlane;
+  constexpr int kStage = TMA ? (G + 1) * kPlane : 0;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[ST + 2];
   __shared__ __align__(16) MapV<V> map[2][kWarps][32];  // against the walk
@@ -855,7 +586,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
       tile_load(dst + b * kPlane, &p.gx, (at.d * G + b) * p.H + at.j0, at.n, t0, bar);
     tile_load(dst + G * kPlane, &p.dy, at.d * p.H + at.j0, at.n, t0, bar);
   };
-  if (threadIdx.x == 0)
+  if (TMA && threadIdx.x == 0)
     for (int r = 0; r < ST; ++r) load(r, r);
   const Words words(warp, at.d);
   const int64_t states_row = (int64_t)p.N * p.D * p.H;
@@ -863,11 +594,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     const int64_t tile = tile_of(r);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      h[v] = r < rounds && active(tile) && at.live ? __ldg(p.states + tile * states_row + at.gh + v) : 0.f;
+      h[v] = r < rounds && active(tile) && v < at.live ? __ldg(p.states + tile * states_row + at.gh + v) : 0.f;
   };
   float carry[V], next[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = at.live && p.dhy ? p.dhy[at.state + v] : 0.f;
+  for (int v = 0; v < V; ++v) carry[v] = v < at.live && p.dhy ? p.dhy[at.state + v] : 0.f;
   state_of(0, next);
   const int64_t tg = (int64_t)p.N * p.ldg * (int64_t)sizeof(E);
   const int64_t step = at.d ? tg : -tg;  // from a step to the one before it
@@ -885,8 +616,29 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = next[v];
     state_of(r + 1, next);
-    if (active(tile)) ring.wait(s, p.status);
+    if (TMA && active(tile)) ring.wait(s, p.status);
     const uint32_t stage = ring.base + s * kStage;
+    // a step's word of plane b (gx: blocks of H; then dy)
+    auto word = [&](int b, int k) -> uint32_t {
+      if constexpr (TMA) {
+        return words.get(stage + b * kPlane, k);
+      } else {
+        const int64_t w = ws + k, t = at.d ? p.T - 1 - w : w;
+        if (!(w >= at.va && w < at.vb)) return 0u;
+        if (b < G)
+          return get_word(static_cast<const E*>(p.gx_at) + (t * p.N + at.n) * p.ldg +
+                              (int64_t)(at.d * G + b) * p.H + at.j, at.live);
+        return get_word(static_cast<const E*>(p.dy_at) + (t * p.N + at.n) * p.ldy +
+                            (int64_t)at.d * p.H + at.j, at.live);
+      }
+    };
+    auto put = [&](char* row, uint32_t w) {
+      if constexpr (TMA) {
+        if (at.live) __stcs(reinterpret_cast<uint32_t*>(row) + lane, w);
+      } else {
+        put_word(reinterpret_cast<E*>(row) + lane * V, w, at.live);
+      }
+    };
     float f[L][V], i[L][V], A[V], B[V], C[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = C[v] = 0.f; }
@@ -894,8 +646,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
       for (int k = 0; k < L; ++k) {
         float pv[V], zv[V];
-        Word<E>::get(words.get(stage, k), pv);
-        Word<E>::get(words.get(stage + kPlane, k), zv);
+        Word<E>::get(word(0, k), pv);
+        Word<E>::get(word(1, k), zv);
         const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -909,8 +661,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
       for (int k = L - 1; k >= 0; --k) {
         float dv[V], q[V];
-        Word<E>::get(words.get(stage + G * kPlane, k), dv);
-        if (GATE) Word<E>::get(words.get(stage + 2 * kPlane, k), q);
+        Word<E>::get(word(G, k), dv);
+        if (GATE) Word<E>::get(word(2, k), q);
         const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -927,7 +679,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
       forth[par][warp][v][lane] = B[v];
     }
     __syncthreads();
-    if (threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
+    if (TMA && threadIdx.x == 0 && r > 0) load(r - 1 + ST, before);
     Chain<V, -1> chain;
     chain.join(map[par], warp, lane);
     MapV<V>* tm = tile_map + par * csize * 32;
@@ -946,7 +698,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 #pragma unroll
         for (int k = 0; k < L; ++k) {
           float zv[V];
-          Word<E>::get(words.get(stage + kPlane, k), zv);
+          Word<E>::get(word(1, k), zv);
           const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
 #pragma unroll
           for (int v = 0; v < V; ++v) {
@@ -969,17 +721,17 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     char* d = d0 + tl * tg;
     if (!on) {
       for (int k = L - 1; k >= 0; --k, d += step)
-        if (at.live && ws + k < p.T)
-          for (int b = 0; b < G; ++b) __stcs(reinterpret_cast<uint32_t*>(d + b * bytes_h) + lane, 0u);
+        if (ws + k < p.T)
+          for (int b = 0; b < G; ++b) put(d + b * bytes_h, 0u);
       continue;
     }
     auto gradients = [&](auto full) {
 #pragma unroll
       for (int k = L - 1; k >= 0; --k, d += step) {
         float zv[V], dv[V], qv[V], gp[V], gz[V], gq[V];
-        Word<E>::get(words.get(stage + kPlane, k), zv);
-        Word<E>::get(words.get(stage + G * kPlane, k), dv);
-        if (GATE) Word<E>::get(words.get(stage + 2 * kPlane, k), qv);
+        Word<E>::get(word(1, k), zv);
+        Word<E>::get(word(G, k), dv);
+        if (GATE) Word<E>::get(word(2, k), qv);
         const bool ok = full.value || (ws + k >= at.va && ws + k < at.vb);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -993,20 +745,20 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
           h[v] = hb[k][v];  // the state after the step before
           c[v] = ok ? f[k][v] * dh : c[v];
         }
-        if (at.live && (full.value || ws + k < p.T)) {
-          uint32_t* o = reinterpret_cast<uint32_t*>(d) + lane;
-          __stcs(o, ok ? Word<E>::put(gp) : 0u);
-          __stcs(reinterpret_cast<uint32_t*>(d + bytes_h) + lane, ok ? Word<E>::put(gz) : 0u);
-          if (GATE) __stcs(reinterpret_cast<uint32_t*>(d + 2 * bytes_h) + lane, ok ? Word<E>::put(gq) : 0u);
+        if (full.value || ws + k < p.T) {
+          put(d, ok ? Word<E>::put(gp) : 0u);
+          put(d + bytes_h, ok ? Word<E>::put(gz) : 0u);
+          if (GATE) put(d + 2 * bytes_h, ok ? Word<E>::put(gq) : 0u);
         }
       }
     };
     if (all) gradients(Yes());
     else gradients(No());
   }
-  if (p.dh0 && rank == 0 && warp == 0 && at.live) {
+  if (p.dh0 && rank == 0 && warp == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) p.dh0[at.state + v] = carry[v];
+    for (int v = 0; v < V; ++v)
+      if (v < at.live) p.dh0[at.state + v] = carry[v];
   }
   if (csize > 1) cluster_sync();
 }
@@ -1058,32 +810,6 @@ __global__ void __launch_bounds__(kThreads) scan_steps_kernel(const ScanP p) {
     for (int v = 0; v < V; ++v) p.hy[l.state + v] = h[v];
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const ScanP& p, int64_t groups, int csize, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * csize));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)csize;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
-}
-
-// Blocks of a cluster share the tiles of a channel group: the smallest power
-// of two (at most 8) that gives the card two blocks an SM, and no more than
-// there are tiles.
-int cluster_for(int64_t groups, int64_t tiles, int num_sms) {
-  int c = 1;
-  while (c < 8 && groups * c < 2 * num_sms && c < tiles) c *= 2;
-  return c;
-}
-
 ScanP params(const ScanArgs& a, int V) {
   ScanP p;
   p.T = a.T; p.N = a.N; p.ldg = a.ldg; p.ldy = a.ldy;
@@ -1095,19 +821,6 @@ ScanP params(const ScanArgs& a, int V) {
   return p;
 }
 
-template <typename E, int V, int CV, int L, bool BWD>
-cudaError_t run(const ScanArgs& a, cudaStream_t st) {
-  using S = Shape<V, CV, L>;
-  const ScanP p = params(a, V);
-  const int64_t groups = (p.vecs + CV - 1) / CV, tiles = (a.T + S::kTile - 1) / S::kTile;
-  const int c = cluster_for(groups, tiles, a.num_sms);
-  if (BWD)
-    return a.gate ? launch(scan_backward_kernel<E, V, CV, L, true>, p, groups, c, st)
-                  : launch(scan_backward_kernel<E, V, CV, L, false>, p, groups, c, st);
-  return a.gate ? launch(scan_forward_kernel<E, V, CV, L, true>, p, groups, c, st)
-                : launch(scan_forward_kernel<E, V, CV, L, false>, p, groups, c, st);
-}
-
 // four channels a load where every row starts on such a boundary
 bool by_four(const ScanArgs& a) {
   const uintptr_t m = a.bf16 ? 8 : 16;
@@ -1116,13 +829,12 @@ bool by_four(const ScanArgs& a) {
          ok(a.dgx);
 }
 
-// TMA's conditions: 16-byte rows, blocks and bases; and channels for at least
-// half a block's width
-bool by_tiles(const ScanArgs& a) {
+// TMA's conditions: rows, blocks of a row and bases on 16 bytes
+bool by_tma(const ScanArgs& a) {
   const int64_t e = a.bf16 ? 2 : 4;
   auto ok = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   return a.H * e % 16 == 0 && a.ldg * e % 16 == 0 && a.ldy * e % 16 == 0 && ok(a.gx) && ok(a.y) &&
-         ok(a.dy) && ok(a.dgx) && a.H * e >= kRow / 2;
+         ok(a.dy) && ok(a.dgx);
 }
 
 template <typename E, typename K>
@@ -1142,16 +854,22 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
     const uint64_t strides[2] = {(uint64_t)ld * sizeof(E), (uint64_t)(a.N * ld) * sizeof(E)};
     return tma_encode(m, 3, a.bf16, ptr, dims, strides, box);
   };
-  if (!map(&p.gx, a.gx, a.D * G * a.H, a.ldg) || (a.dy && !map(&p.dy, a.dy, a.D * a.H, a.ldy)))
+  p.gx_at = a.gx;
+  p.dy_at = a.dy;
+  if (stages && (!map(&p.gx, a.gx, a.D * G * a.H, a.ldg) || (a.dy && !map(&p.dy, a.dy, a.D * a.H, a.ldy))))
     return cudaErrorInvalidValue;
-  // blocks of a cluster share a channel group's tiles where the groups alone
-  // give the card less than two blocks an SM
+  // Blocks of a cluster share a channel group's tiles where the groups alone give
+  // the card less than two blocks an SM.  65536 x 1 x 1024 forward takes 158 us
+  // with clusters of 16; with eight warps a tile 232 us (two blocks an SM hold 14
+  // such clusters, not 16).
   const int64_t groups = a.N * a.D * p.groups_h, tiles = (a.T + kTileSteps - 1) / kTileSteps;
   int csize = 1;
   while (csize < 16 && groups * csize < 2 * a.num_sms && csize < tiles) csize *= 2;
   const size_t smem = (size_t)stages * planes * kPlane + 1024 +
                       (csize > 1 ? 2 * csize * 32 * sizeof(MapV<Word<E>::V>) : 0);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess && csize > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
@@ -1165,7 +883,7 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
   at[0].val.clusterDim.x = (unsigned)csize;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = csize > 1 ? 1 : 0;  // a launch with the attribute takes 2 us longer
   e = cudaLaunchKernelEx(&cfg, kernel, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   return e;
@@ -1174,15 +892,17 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
 // Stages of the ring: two tiles in flight a block.  A third leaves room for
 // two blocks an SM instead of three and measured slower (65536 x 1 x 1024
 // forward 158 -> 222 us, 512 x 128 x 1024 training 353 -> 386 us).
-template <typename E>
+template <typename E, bool GATE>
 cudaError_t forward_tiles(const ScanArgs& a, cudaStream_t st) {
-  return a.gate ? run_tiles<E>(scan_forward_tiles<E, true, 2>, a, 3, 2, st)
-                : run_tiles<E>(scan_forward_tiles<E, false, 3>, a, 2, 3, st);
+  constexpr int planes = GATE ? 3 : 2, stages = GATE ? 2 : 3;
+  if (!by_tma(a)) return run_tiles<E>(scan_forward_tiles<E, GATE, false, 1>, a, 0, 0, st);
+  return run_tiles<E>(scan_forward_tiles<E, GATE, true, stages>, a, planes, stages, st);
 }
-template <typename E>
+template <typename E, bool GATE>
 cudaError_t backward_tiles(const ScanArgs& a, cudaStream_t st) {
-  return a.gate ? run_tiles<E>(scan_backward_tiles<E, true, 2>, a, 4, 2, st)
-                : run_tiles<E>(scan_backward_tiles<E, false, 2>, a, 3, 2, st);
+  constexpr int planes = GATE ? 4 : 3;
+  if (!by_tma(a)) return run_tiles<E>(scan_backward_tiles<E, GATE, false, 1>, a, 0, 0, st);
+  return run_tiles<E>(scan_backward_tiles<E, GATE, true, 2>, a, planes, 2, st);
 }
 
 template <typename E, int V>
@@ -1198,22 +918,17 @@ cudaError_t forward_steps(const ScanArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t scan_forward(const ScanArgs& a, cudaStream_t st) {
-  const bool four = by_four(a);
   if (a.T <= 8) {
-    if (four) return a.bf16 ? forward_steps<bf16, 4>(a, st) : forward_steps<float, 4>(a, st);
+    if (by_four(a)) return a.bf16 ? forward_steps<bf16, 4>(a, st) : forward_steps<float, 4>(a, st);
     return a.bf16 ? forward_steps<bf16, 1>(a, st) : forward_steps<float, 1>(a, st);
   }
-  if (by_tiles(a)) return a.bf16 ? forward_tiles<bf16>(a, st) : forward_tiles<float>(a, st);
-  if (four)
-    return a.bf16 ? run<bf16, 4, 16, 8, false>(a, st) : run<float, 4, 16, 8, false>(a, st);
-  return a.bf16 ? run<bf16, 1, 32, 16, false>(a, st) : run<float, 1, 32, 16, false>(a, st);
+  if (a.bf16) return a.gate ? forward_tiles<bf16, true>(a, st) : forward_tiles<bf16, false>(a, st);
+  return a.gate ? forward_tiles<float, true>(a, st) : forward_tiles<float, false>(a, st);
 }
 
 cudaError_t scan_backward(const ScanArgs& a, cudaStream_t st) {
-  if (by_tiles(a)) return a.bf16 ? backward_tiles<bf16>(a, st) : backward_tiles<float>(a, st);
-  if (by_four(a))
-    return a.bf16 ? run<bf16, 4, 16, 8, true>(a, st) : run<float, 4, 16, 4, true>(a, st);
-  return a.bf16 ? run<bf16, 1, 32, 8, true>(a, st) : run<float, 1, 32, 8, true>(a, st);
+  if (a.bf16) return a.gate ? backward_tiles<bf16, true>(a, st) : backward_tiles<bf16, false>(a, st);
+  return a.gate ? backward_tiles<float, true>(a, st) : backward_tiles<float, false>(a, st);
 }
 
 }  // namespace lr
