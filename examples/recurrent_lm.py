@@ -1,0 +1,212 @@
+"""A small recurrent language model of gated linear recurrences and gated
+feed-forwards: trained in float32 or bfloat16, then answering token by token with
+4-bit weights.
+
+    python examples/recurrent_lm.py [--dtype bf16] [--steps 300]
+
+The task is made up: a sequence's first token is a key k, and every later token is
+the one before plus k (modulo the vocabulary), so that the state has to hold the
+key.  A layer is
+
+    h <- h + scan(norm(h) Wg^T) Wo^T      gated linear recurrence, output gate
+    h <- h + glu(norm(h), Wu) Wd^T        gated feed-forward
+
+The recurrence and the feed-forward are the library's, forward and backward; the
+plain projections of training are matrix products of torch.  Generation keeps one
+float32 state a layer and calls the one-step recurrence, the few-row
+feed-forward and the 4-bit products.
+"""
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+from layer_rnn_gb300 import binding  # noqa: E402
+
+GROUP = 32
+
+
+class Scan(torch.autograd.Function):
+    """gx [T, N, 3 H] -> y [T, N, H], from a zero state."""
+
+    @staticmethod
+    def forward(ctx, gx, ops):
+        T, N, width = gx.shape
+        H = width // 3
+        y = gx.new_empty((T, N, H))
+        ws = torch.empty(ops.scan_workspace_bytes(T, N, H), dtype=torch.uint8, device=gx.device)
+        ops.scan_forward(gx, None, y, None, ws=ws, out_gate=True)
+        ctx.save_for_backward(gx, ws)
+        ctx.ops = ops
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        gx, ws = ctx.saved_tensors
+        dgx = torch.empty_like(gx)
+        ctx.ops.scan_backward(gx, dy.contiguous(), None, dgx, None, ws, out_gate=True)
+        return dgx, None
+
+
+class Glu(torch.autograd.Function):
+    """x [M, K], W [2 F, K] -> silu(x Wg^T) * (x Wu^T) [M, F]."""
+
+    @staticmethod
+    def forward(ctx, x, W, ops):
+        M, K, F = x.shape[0], x.shape[1], W.shape[0] // 2
+        y = x.new_empty((M, F))
+        # the backward's workspace serves both
+        ws = torch.empty(ops.glu_workspace_bytes(M, K, F, backward=True), dtype=torch.uint8,
+                         device=x.device)
+        ops.glu_forward(x, W, y, ws)
+        ctx.save_for_backward(x, W)
+        ctx.ws, ctx.ops = ws, ops
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, W = ctx.saved_tensors
+        dx, dW = torch.empty_like(x), torch.empty_like(W)
+        ctx.ops.glu_backward(x, W, dy.contiguous(), dx, dW, ctx.ws)
+        return dx, dW, None
+
+
+def norm(h):
+    return (h.float() * torch.rsqrt(h.float().square().mean(-1, keepdim=True) + 1e-6)).to(h.dtype)
+
+
+class Model:
+    def __init__(self, ops, vocab=32, width=128, H=128, F=256, layers=2, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+
+        def weight(rows, cols):
+            w = torch.randn((rows, cols), generator=gen, device="cuda") / cols ** 0.5
+            return w.to(ops.tdtype).requires_grad_()
+
+        self.ops, self.vocab, self.H, self.F = ops, vocab, H, F
+        self.embed = weight(vocab, width)
+        self.layers = [dict(gates=weight(3 * H, width), out=weight(width, H), up=weight(2 * F, width),
+                            down=weight(width, F)) for _ in range(layers)]
+        with torch.no_grad():
+            for k, layer in enumerate(self.layers):  # rows scaled apart: some gates remember long
+                layer["gates"][:H] *= 2.0
+
+    def parameters(self):
+        return [self.embed] + [w for layer in self.layers for w in layer.values()]
+
+    def logits(self, tokens):
+        """tokens [T, N] -> logits [T, N, vocab]."""
+        T, N = tokens.shape
+        h = self.embed[tokens]
+        for layer in self.layers:
+            h = h + Scan.apply(norm(h) @ layer["gates"].t(), self.ops) @ layer["out"].t()
+            x = norm(h).reshape(T * N, -1)
+            h = h + (Glu.apply(x, layer["up"], self.ops) @ layer["down"].t()).view_as(h)
+        return norm(h) @ self.embed.t()
+
+
+class Generator:
+    """The trained model with 4-bit projections, one token of N sequences a call."""
+
+    def __init__(self, model, N):
+        ops, F, H = model.ops, model.F, model.H
+        self.model, self.ops, self.N = model, ops, N
+
+        def four_bits(w):
+            R, K = w.shape
+            q, s, z = ops.w4_alloc(R, K, GROUP, zeros=True)
+            ops.w4_quantize(w.detach().contiguous(), q, s, GROUP, z)
+            return q, s, z
+
+        self.layers = [{k: four_bits(w) for k, w in layer.items() if k != "up"} for layer in model.layers]
+        self.head = four_bits(model.embed)
+        # the fixed buffers of a step
+        new = lambda cols: torch.empty((N, cols), dtype=ops.tdtype, device="cuda")  # noqa: E731
+        width = model.embed.shape[1]
+        self.gx, self.y, self.f, self.add, self.out = new(3 * H), new(H), new(F), new(width), new(model.vocab)
+        self.states = [torch.zeros((N, H), device="cuda") for _ in model.layers]
+        self.ws = torch.empty(ops.glu_workspace_bytes(N, width, F), dtype=torch.uint8, device="cuda")
+
+    def product(self, x, w, y):
+        q, s, z = w
+        self.ops.w4_matvec(x, q, s, y, GROUP, z)
+        return y
+
+    def step(self, tokens):
+        """tokens [N] -> logits [N, vocab] (a buffer that the next step reuses)."""
+        h = self.model.embed.detach()[tokens]
+        for layer, four, state in zip(self.model.layers, self.layers, self.states):
+            self.product(norm(h), four["gates"], self.gx)
+            self.ops.scan_step(self.gx, state, state, self.y, out_gate=True)
+            h = h + self.product(self.y, four["out"], self.add)
+            self.ops.glu_forward(norm(h), layer["up"].detach(), self.f, self.ws)
+            h = h + self.product(self.f, four["down"], self.add)
+        return self.product(norm(h), self.head, self.out)
+
+
+def sequences(gen, vocab, T, N):
+    """[T, N]: key, start, start + key, start + 2 key, ..."""
+    key = torch.randint(1, vocab, (1, N), generator=gen, device="cuda")
+    start = torch.randint(0, vocab, (1, N), generator=gen, device="cuda")
+    rest = (start + key * torch.arange(T - 1, device="cuda")[:, None]) % vocab
+    return torch.cat([key, rest])
+
+
+def train(model, steps, T=48, N=64, lr=3e-3, seed=1):
+    """Adam on float32 copies of the weights; returns the first and the last loss."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    params = model.parameters()
+    master = [p.detach().float().clone() for p in params]
+    first = last = None
+    opt = torch.optim.Adam(master, lr=lr)
+    for _ in range(steps):
+        tokens = sequences(gen, model.vocab, T, N)
+        logits = model.logits(tokens[:-1]).float()
+        # the second token is not to be known: the loss starts at the third
+        loss = torch.nn.functional.cross_entropy(logits[1:].reshape(-1, model.vocab), tokens[2:].reshape(-1))
+        loss.backward()
+        for m, p in zip(master, params):
+            m.grad = p.grad.float()
+            p.grad = None
+        opt.step()
+        with torch.no_grad():
+            for m, p in zip(master, params):
+                p.copy_(m)
+        last = loss.detach()
+        first = last if first is None else first
+    return first.item(), last.item()
+
+
+def generate(model, N=16, length=24, seed=2):
+    """Share of generated tokens that follow the rule, from a key and a start."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    want = sequences(gen, model.vocab, length + 2, N)
+    g = Generator(model, N)
+    g.step(want[0])
+    token = want[1]
+    right = torch.zeros((), device="cuda")
+    for t in range(length):
+        token = g.step(token).float().argmax(-1)
+        right += (token == want[2 + t]).float().mean()
+    return (right / length).item()
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--dtype", choices=("f32", "bf16"), default="f32")
+    ap.add_argument("--steps", type=int, default=400)
+    a = ap.parse_args(argv)
+    model = Model(binding.Ops(a.dtype))
+    first, last = train(model, a.steps)
+    share = generate(model)
+    print("loss %.3f -> %.3f in %d steps; %.0f %% of the tokens generated with 4-bit weights follow the rule"
+          % (first, last, a.steps, 100 * share))
+    return first, last, share
+
+
+if __name__ == "__main__":
+    main()

@@ -178,6 +178,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int e = warp - 2, q = warp & 3, half = e >> 2;
     const uint32_t box0 = base + (uint32_t)(ST * kStage + e * kBoxes * kBox);
     const uint32_t tempty = map_rank(tempty0, 0);
+    // dy of a tile is loaded while the one before is finished
+    auto load_dy = [&](const Walk& of) {
+      int z, mt, nt;
+      tile_at(p, of.tile, z, mt, nt);
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(dy0 + 8 * e, kBox);
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box0 + kBox),
+            "l"(reinterpret_cast<uint64_t>(&maps.dy)), "r"(nt * kHalf + half * 64),
+            "r"(mt * kTile + (int)rank * kHalf + q * 32), "r"(0), "r"(dy0 + 8 * e)
+            : "memory");
+      }
+    };
+    if (PROD == kDgu && p.tma_dy) {
+      Walk ahead = w;
+      if (walk_next(p, ahead, pair, pairs)) load_dy(ahead);
+    }
     uint32_t dy_ph = 0;
     int n = 0;
     while (walk_next(p, w, pair, pairs)) {
@@ -187,20 +205,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row0 = mt * kTile + (int)rank * kHalf + q * 32;
       const uint32_t lanes = tmem + (uint32_t)(buf * 256) + ((uint32_t)(q * 32) << 16);
       const int f0 = nt * kHalf + half * 64;  // first feature of a gated tile
-      if (PROD == kDgu && p.tma_dy) {
-        // dy under the product: its box is free once du, stored from it, has been read
-        if (lane == 0) {
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          tc::mbar_arrive_expect_tx(dy0 + 8 * e, kBox);
-          asm volatile(
-              "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-              " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box0 + kBox),
-              "l"(reinterpret_cast<uint64_t>(&maps.dy)), "r"(f0), "r"(row0), "r"(0),
-              "r"(dy0 + 8 * e)
-              : "memory");
-        }
-        __syncwarp();
-      }
       if (!__all_sync(0xffffffffu, wait_phase<false>(tfull0 + 8 * buf, (n >> 1) & 1, p.status)))
         break;
       tc::fence_after();
@@ -231,7 +235,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
         const uint32_t row_at = box0 + (uint32_t)lane * 128u;
-#pragma unroll 1
+        uint32_t up[PROD == kDgu ? 32 : 1];  // du, until dg has left the box
+#pragma unroll
         for (int c = 0; c < 64; c += 32) {
           float g[32], u[32];
           tc::tmem_ld32(lanes + (uint32_t)(half * 64 + c), g);
@@ -244,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t piece = (uint32_t)(((c >> 3) + j) ^ (lane & 7)) << 4;
-            uint32_t o[4], o2[4];
+            uint32_t o[4];
             uint4 dv = make_uint4(0, 0, 0, 0);
             if (PROD == kDgu) {
               if (p.tma_dy) {
@@ -275,16 +280,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 glu::value_slope(g[k], ACT, v0, d0);
                 glu::value_slope(g[k + 1], ACT, v1, d1);
                 o[i] = glu::pack2(y0 * u[k] * d0, y1 * u[k + 1] * d1);
-                o2[i] = glu::pack2(y0 * v0, y1 * v1);
+                up[PROD == kDgu ? c / 2 + 4 * j + i : 0] = glu::pack2(y0 * v0, y1 * v1);
               }
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + piece), "r"(o[0]),
                          "r"(o[1]), "r"(o[2]), "r"(o[3])
                          : "memory");
-            if (PROD == kDgu)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + kBox + piece),
-                           "r"(o2[0]), "r"(o2[1]), "r"(o2[2]), "r"(o2[3])
-                           : "memory");
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -292,8 +293,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (p.tma_out) {
           if (lane == 0 && row0 < p.rows && f0 < p.cols) {
             store_box(&maps.out, box0, f0, row0, 0);
-            if (PROD == kDgu) store_box(&maps.out, box0 + kBox, f0, row0, 1);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          if (PROD == kDgu) {
+            if (p.tma_dy) {
+              Walk ahead = w;
+              if (walk_next(p, ahead, pair, pairs)) load_dy(ahead);
+            }
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t* v = up + (PROD == kDgu ? 4 * j : 0);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               row_at + ((uint32_t)(j ^ (lane & 7)) << 4)),
+                           "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                           : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && row0 < p.rows && f0 < p.cols) {
+              store_box(&maps.out, box0, f0, row0, 1);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
           }
         } else {
           glu::store_rows(box0, static_cast<bf16*>(p.out), p.ld_out, row0, f0, p.rows, p.cols, lane);
@@ -395,9 +417,7 @@ cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st)
   e = cudaGetLastError();
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
-  glu_join_kernel<bf16, kTile><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError();
+  return launch_join<bf16, kTile>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
 cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {

@@ -36,10 +36,11 @@ constexpr int kStage = 2 * (kA + kB);
 constexpr int ST = 3;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kSmem = ST * kStage + 1024;
+constexpr int kBox = 32 * 128;         // an epilogue warp's 32 rows of 32 results
+constexpr int kSmem = ST * kStage + kEpiWarps * kBox + 1024;
 
 struct Maps {
-  CUtensorMap ah, al, bh, bl;
+  CUtensorMap ah, al, bh, bl, out, dy;
 };
 
 // the scale that maps the largest magnitude (bit pattern mb) into
@@ -59,14 +60,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // kind::f16, fp16 operands, float32 sums, M = 256, N = 256
   constexpr uint32_t kIdesc = (1u << 4) | ((kAmn ? 1u : 0u) << 15) | ((kBmn ? 1u : 0u) << 16) |
                               ((uint32_t)(kCols >> 3) << 17) | ((uint32_t)(2 * kHalf >> 4) << 24);
-  __shared__ __align__(8) uint64_t bars[2 * ST + 4];
+  __shared__ __align__(8) uint64_t bars[2 * ST + 4 + kEpiWarps];
   __shared__ uint32_t tmem_slot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned rank = tc::cl_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const uint32_t base = (tc::smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t full0 = tc::smem_addr(&bars[0]), empty0 = full0 + 8 * ST;
-  const uint32_t tfull0 = empty0 + 8 * ST, tempty0 = tfull0 + 16;
+  const uint32_t tfull0 = empty0 + 8 * ST, tempty0 = tfull0 + 16, dy0 = tempty0 + 16;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
@@ -77,6 +78,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(tfull0 + 8 * i, 1);
       tc::mbar_init(tempty0 + 8 * i, 2 * kEpiWarps);
     }
+    for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(dy0 + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 2) {
@@ -184,14 +186,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tempty = map_rank(tempty0, 0);
     const float ia = unscale(*p.amax), ib = unscale(*p.bmax);
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    const bool vec = p.tma_out != 0;  // rows of float4
+    // results leave through a box of 32 rows x 32 columns in shared memory (16-byte
+    // piece j of row r at piece j ^ (r & 7)): stores by rows of a lane each took as
+    // long as the MMAs of the next tile
+    const uint32_t box = base + (uint32_t)(ST * kStage + e * kBox);
+    const uint32_t row_at = box + (uint32_t)lane * 128u;
+    auto piece = [&](int j) { return row_at + ((uint32_t)(j ^ (lane & 7)) << 4); };
+    auto box_free = [&] {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
+    // 32 columns of a lane's row to (plane, row0 + lane, col)
+    auto put = [&](const float* v, int plane, int row0, int col) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(piece(j)), "f"(v[4 * j]),
+                     "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                     : "memory");
+      if (p.tma_out) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0 && row0 < p.rows && col < p.cols) {
+          store_box(&maps.out, box, col, row0, plane);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      } else {
+        __syncwarp();
+        float* o = static_cast<float*>(p.out) + ((int64_t)plane * p.rows + row0) * p.ld_out + col + lane;
+        if (col + lane < p.cols)
+          for (int r = 0; r < 32 && row0 + r < p.rows; ++r) {
+            float f;
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(f)
+                         : "r"(box + (uint32_t)(r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4))
+                         : "memory");
+            o[(int64_t)r * p.ld_out] = f;
+          }
+        __syncwarp();
+      }
+    };
+    uint32_t dy_ph = 0;
+    auto load_dy = [&](int row0, int col) {
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(dy0 + 8 * e, kBox);
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box),
+            "l"(reinterpret_cast<uint64_t>(&maps.dy)), "r"(col), "r"(row0), "r"(0), "r"(dy0 + 8 * e)
+            : "memory");
+      }
+    };
     unsigned mx = 0;
     int blk = 0, n = 0;
     bool ok = true;
     while (ok && walk_next(p, w, pair, pairs)) {
-      __syncwarp();  // rows past the end skip their stores
       int z, mt, nt;
       tile_at(p, w.tile, z, mt, nt);
+      const int row0 = mt * 2 * kHalf + (int)rank * kHalf + q * 32, f0 = nt * kHalf + half * 64;
+      if (PROD == kDgu && p.tma_dy) {  // under the products
+        box_free();
+        load_dy(row0, f0);
+      }
       float s0[64], s1[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) s0[i] = s1[i] = 0.f;
@@ -241,58 +296,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      const int row = mt * 2 * kHalf + (int)rank * kHalf + q * 32 + lane;
-      if (row >= p.rows) continue;
-      auto put = [&](const float (&v)[64], int plane, int col) {
-        float* o = static_cast<float*>(p.out) + ((int64_t)plane * p.rows + row) * p.ld_out + col;
+      if constexpr (!kGated) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float f[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
-          if (vec && col + 4 * i < p.cols) store4(o + 4 * i, f);
-          if (!vec)
-            for (int u = 0; u < 4; ++u)
-              if (col + 4 * i + u < p.cols) o[4 * i + u] = f[u];
+        for (int h = 0; h < 2; ++h) {
+          box_free();
+          put(s0 + 32 * h, z, row0, nt * kCols + c0 + 32 * h);
         }
-      };
-      if (!kGated) {
-        put(s0, z, nt * kCols + c0);
-        put(s1, z, nt * kCols + c1);
-        continue;
-      }
-      const int f0 = nt * kHalf + half * 64;
-      if (PROD == kForward) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) s0[i] = value(s0[i], ACT) * s1[i];
-        put(s0, 0, f0);
+        for (int h = 0; h < 2; ++h) {
+          box_free();
+          put(s1 + 32 * h, z, row0, nt * kCols + c1 + 32 * h);
+        }
       } else {
-        const float* dy = static_cast<const float*>(p.dy) + (int64_t)row * p.ld_dy + f0;
-        const bool dvec = p.tma_dy != 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (dvec) {
-            if (f0 + 4 * i < p.cols) y = __ldg(reinterpret_cast<const float4*>(dy + 4 * i));
+        for (int h = 0; h < 2; ++h) {
+          const int col = f0 + 32 * h;
+          if (PROD == kForward) {
+#pragma unroll
+            for (int i = 32 * h; i < 32 * h + 32; ++i) s0[i] = value(s0[i], ACT) * s1[i];
           } else {
-            if (f0 + 4 * i < p.cols) y.x = __ldg(dy + 4 * i);
-            if (f0 + 4 * i + 1 < p.cols) y.y = __ldg(dy + 4 * i + 1);
-            if (f0 + 4 * i + 2 < p.cols) y.z = __ldg(dy + 4 * i + 2);
-            if (f0 + 4 * i + 3 < p.cols) y.w = __ldg(dy + 4 * i + 3);
-          }
-          const float yv[4] = {y.x, y.y, y.z, y.w};
+            if (p.tma_dy) {
+              if (h > 0) {
+                box_free();
+                load_dy(row0, col);
+              }
+              if (!__all_sync(0xffffffffu, wait_phase<false>(dy0 + 8 * e, dy_ph, p.status))) {
+                ok = false;
+                break;
+              }
+              dy_ph ^= 1u;
+            }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float v, d;
-            value_slope(s0[4 * i + u], ACT, v, d);
-            s0[4 * i + u] = yv[u] * s1[4 * i + u] * d;
-            s1[4 * i + u] = yv[u] * v;
-            mx = max(mx, max(__float_as_uint(s0[4 * i + u]) & 0x7fffffffu,
-                             __float_as_uint(s1[4 * i + u]) & 0x7fffffffu));
+            for (int j = 0; j < 8; ++j) {
+              float y[4] = {0.f, 0.f, 0.f, 0.f};
+              if (p.tma_dy) {
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(y[0]), "=f"(y[1]), "=f"(y[2]), "=f"(y[3])
+                             : "r"(piece(j))
+                             : "memory");
+              } else if (row0 + lane < p.rows) {
+                const float* dy = static_cast<const float*>(p.dy) + (int64_t)(row0 + lane) * p.ld_dy + col + 4 * j;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (col + 4 * j + u < p.cols) y[u] = __ldg(dy + u);
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int i = 32 * h + 4 * j + u;
+                float v, d;
+                value_slope(s0[i], ACT, v, d);
+                s0[i] = y[u] * s1[i] * d;
+                s1[i] = y[u] * v;
+                mx = max(mx, max(__float_as_uint(s0[i]) & 0x7fffffffu, __float_as_uint(s1[i]) & 0x7fffffffu));
+              }
+            }
+          }
+          if (PROD == kForward || !p.tma_dy) box_free();
+          __syncwarp();
+          put(s0 + 32 * h, 0, row0, col);
+          if (PROD == kDgu) {
+            box_free();
+            put(s1 + 32 * h, 1, row0, col);
           }
         }
-        put(s0, 0, f0);
-        put(s1, 1, f0);
       }
+      if (!ok) break;
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (PROD == kDgu) {
       __syncwarp();
       mx = __reduce_max_sync(0xffffffffu, mx);
@@ -315,16 +385,13 @@ cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const int pairs = plan_pairs(&p, a.num_sms, 8);  // 256 KB each way, three products a block
   p.group = std::min(p.m_tiles, 16);
-  p.tma_out = p.ld_out % 4 == 0 && p.cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
   p.status = a.status;
   kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
   g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
   e = cudaGetLastError();
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
-  glu_join_kernel<float, kCols><<<(unsigned)(cut_tiles * 8), 256, 0, st>>>(p, pairs);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError();
+  return launch_join<float, kCols>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
 cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
@@ -363,6 +430,15 @@ struct Room {
     const cudaError_t e_ = (call); \
     if (e_ != cudaSuccess) return e_; \
   } while (0)
+
+// float32 map: boxes of 32 x 32
+bool map_f32(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t planes, int64_t ld) {
+  if (ld % 4 != 0 || reinterpret_cast<uintptr_t>(ptr) % 16 != 0) return false;
+  const uint64_t dims[3] = {(uint64_t)cols, (uint64_t)rows, (uint64_t)planes};
+  const uint64_t strides[2] = {(uint64_t)ld * 4, (uint64_t)(ld * rows) * 4};
+  const uint32_t box[3] = {32u, 32u, 1u};
+  return tma_encode(m, 3, false, ptr, dims, strides, box);
+}
 
 // src [rows][cols], row pitch lds, to pairs, with the scale of *mx
 cudaError_t split(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& q,
@@ -418,6 +494,7 @@ cudaError_t glu_f32_forward(const GluArgs& a, cudaStream_t st) {
   if (!gated_maps(a, x, w, &maps)) return cudaErrorInvalidValue;
   P p = gated(a, mx);
   p.out = a.y; p.ld_out = a.F;
+  p.tma_out = map_f32(&maps.out, a.y, a.F, a.M, 1, a.F);
   return launch<kForward>(maps, p, a, st);
 }
 
@@ -435,8 +512,9 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     if (!gated_maps(a, x, w, &maps)) return cudaErrorInvalidValue;
     P p = gated(a, mx);
     p.dy = a.dy; p.ld_dy = a.F;
-    p.tma_dy = a.F % 4 == 0;
+    p.tma_dy = map_f32(&maps.dy, a.dy, a.F, a.M, 1, a.F);
     p.out = dgu; p.ld_out = Fp;
+    p.tma_out = map_f32(&maps.out, dgu, a.F, a.M, 2, Fp);
     p.omax = mx + 2;
     TRY(launch<kDgu>(maps, p, a, st));
   }
@@ -460,6 +538,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.nkb = 2 * p.kb_plane;
     p.rows = (int)a.M;
     p.out = a.dx;
+    p.tma_out = map_f32(&m.out, a.dx, a.K, a.M, 1, a.K);
     p.bmax = mx + 1;
     TRY(launch<kDx>(m, p, a, st));
   }
@@ -476,6 +555,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.nkb = (int)ceil_div(a.M, 64);
     p.rows = (int)a.F;
     p.out = a.dW;
+    p.tma_out = map_f32(&m.out, a.dW, a.K, a.F, 2, a.K);
     p.bmax = mx;
     TRY(launch<kDw>(m, p, a, st));
   }

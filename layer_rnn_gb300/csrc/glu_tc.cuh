@@ -188,12 +188,14 @@ __device__ __forceinline__ float4* part_at(const P& p, int64_t slot, int part) {
   return reinterpret_cast<float4*>(p.part) + (slot * 8 + part) * (TN / 4 * 32);
 }
 
-// Joins the partial tiles: block x handles one cut tile's eighth (block of the
-// pair * 4 + row quarter).  Pairs in rising order.
+// Joins the partial tiles: block x handles four columns of 32 rows for each of its
+// warps, in one cut tile's eighth (block of the pair * 4 + row quarter).  Pairs in
+// rising order.
 template <typename E, int TN>
 __global__ void __launch_bounds__(256) glu_join_kernel(const P p, int pairs) {
-  const int part = blockIdx.x & 7;
-  const int rel = blockIdx.x >> 3, tile = p.whole + rel;
+  constexpr int kBlocks = TN / 4 * 32 / 256;  // of an eighth
+  const int part = blockIdx.x / kBlocks & 7;
+  const int rel = blockIdx.x / kBlocks >> 3, tile = p.whole + rel;
   int z, mt, nt;
   tile_at(p, tile, z, mt, nt);
   const Cut c(p);
@@ -205,23 +207,28 @@ __global__ void __launch_bounds__(256) glu_join_kernel(const P p, int pairs) {
   const int row0 = mt * 2 * kHalf + (part >> 2) * kHalf + (part & 3) * 32;
   E* out = static_cast<E*>(p.out);
   const bool by_four = p.ld_out % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(E)) == 0;
-  for (int i = threadIdx.x; i < TN / 4 * 32; i += 256) {
-    float4 s = __ldcs(part_at<TN>(p, rel, part) + i);
-    for (int j = first; j < pairs - c.left && c.begin(j, pairs) < t1; ++j) {
-      if (c.begin(j + 1, pairs) == c.begin(j, pairs)) continue;
-      const float4 v = __ldcs(part_at<TN>(p, c.left + j + rel, part) + i);
-      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-    }
-    const int row = row0 + (i & 31), col = nt * TN + (i >> 5) * 4;
-    if (row >= p.rows || col >= p.cols) continue;
-    E* o = out + ((int64_t)z * p.rows + row) * p.ld_out + col;
-    const float v[4] = {s.x, s.y, s.z, s.w};
-    if (by_four && col + 4 <= p.cols) {
-      store4(o, v);
-    } else {
-      for (int u = 0; u < 4 && col + u < p.cols; ++u) o[u] = from_f<E>(v[u]);
-    }
+  const int i = blockIdx.x % kBlocks * 256 + threadIdx.x;
+  float4 s = __ldcs(part_at<TN>(p, rel, part) + i);
+  for (int j = first; j < pairs - c.left && c.begin(j, pairs) < t1; ++j) {
+    if (c.begin(j + 1, pairs) == c.begin(j, pairs)) continue;
+    const float4 v = __ldcs(part_at<TN>(p, c.left + j + rel, part) + i);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
+  const int row = row0 + (i & 31), col = nt * TN + (i >> 5) * 4;
+  if (row >= p.rows || col >= p.cols) return;
+  E* o = out + ((int64_t)z * p.rows + row) * p.ld_out + col;
+  const float v[4] = {s.x, s.y, s.z, s.w};
+  if (by_four && col + 4 <= p.cols) {
+    store4(o, v);
+  } else {
+    for (int u = 0; u < 4 && col + u < p.cols; ++u) o[u] = from_f<E>(v[u]);
+  }
+}
+template <typename E, int TN>
+cudaError_t launch_join(const P& p, int64_t cut_tiles, int pairs, cudaStream_t st) {
+  glu_join_kernel<E, TN><<<(unsigned)(cut_tiles * 8 * (TN / 4 * 32 / 256)), 256, 0, st>>>(p, pairs);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError();
 }
 
 // Pairs of blocks at work, and how many tiles (p.whole) they do whole.  Tiles
