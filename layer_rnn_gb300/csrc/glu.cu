@@ -61,8 +61,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   constexpr bool kAmn = PROD == kDw, kBmn = PROD == kDx || PROD == kDw;
   constexpr bool kGated = PROD == kForward || PROD == kDgu;
-  constexpr int kBoxes = PROD == kDgu ? 2 : 1;  // staging boxes of an epilogue warp
-  constexpr int ST = (kSmem - 1024 - kEpiWarps * kBoxes * kBox) / kStage;
+  // One box an epilogue warp, through which dy, dg and du of the backward go in
+  // turn, so that six stages fit: with five and a box for dy it took 719 us where
+  // this takes 677, with four and three boxes 779 (65536 x 1024 x 4096).
+  constexpr int ST = (kSmem - 1024 - kEpiWarps * kBox) / kStage;
   // kind::f16, bf16 operands, float32 sums, M = 256, N = 256
   constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((kAmn ? 1u : 0u) << 15) |
                               ((kBmn ? 1u : 0u) << 16) | ((uint32_t)(kTile >> 3) << 17) |
@@ -176,9 +178,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // epilogue: warp e takes lanes (rows) 32 (warp % 4) and half e / 4 of the
     // columns (of the features, where gate and up columns belong together)
     const int e = warp - 2, q = warp & 3, half = e >> 2;
-    const uint32_t box0 = base + (uint32_t)(ST * kStage + e * kBoxes * kBox);
+    const uint32_t box0 = base + (uint32_t)(ST * kStage + e * kBox);
     const uint32_t tempty = map_rank(tempty0, 0);
-    // dy of a tile is loaded while the one before is finished
+    // dy of a tile is loaded once du of the one before has left the box
     auto load_dy = [&](const Walk& of) {
       int z, mt, nt;
       tile_at(p, of.tile, z, mt, nt);
@@ -186,7 +188,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::mbar_arrive_expect_tx(dy0 + 8 * e, kBox);
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box0 + kBox),
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(box0),
             "l"(reinterpret_cast<uint64_t>(&maps.dy)), "r"(nt * kHalf + half * 64),
             "r"(mt * kTile + (int)rank * kHalf + q * 32), "r"(0), "r"(dy0 + 8 * e)
             : "memory");
@@ -232,8 +234,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           dy_ph ^= 1u;
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
+        if (PROD == kForward || !p.tma_dy) {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
         const uint32_t row_at = box0 + (uint32_t)lane * 128u;
         uint32_t up[PROD == kDgu ? 32 : 1];  // du, until dg has left the box
 #pragma unroll
@@ -255,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (p.tma_dy) {
                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(dv.x), "=r"(dv.y), "=r"(dv.z), "=r"(dv.w)
-                             : "r"(row_at + kBox + piece));
+                             : "r"(row_at + piece));
               } else {
                 uint32_t h[8];
 #pragma unroll
@@ -296,10 +300,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
           if (PROD == kDgu) {
-            if (p.tma_dy) {
-              Walk ahead = w;
-              if (walk_next(p, ahead, pair, pairs)) load_dy(ahead);
-            }
             if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             __syncwarp();
 #pragma unroll
@@ -315,6 +315,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0 && row0 < p.rows && f0 < p.cols) {
               store_box(&maps.out, box0, f0, row0, 1);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            Walk ahead = w;
+            if (p.tma_dy && walk_next(p, ahead, pair, pairs)) {
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+              __syncwarp();
+              load_dy(ahead);
             }
           }
         } else {

@@ -9,7 +9,7 @@
 // product is free: a lane's 16-byte piece of a row goes from memory into the
 // registers that are the operand, four steps ahead of its use, with no shared
 // memory or barrier between.  (A ring of asynchronous copies took 7.3 us where
-// this takes GLUTOKEN: one token, 1024 x 4096.)
+// this takes 6.5: one token, 1024 x 4096, weights from memory.)
 // bfloat16: m16n8k16.  float32: m16n8k8 in tf32, three products, v = hi + lo with
 // hi the upper 11 bits: 22 bits an operand; the products of 32 k are added to sums
 // in float32, which round to nearest (the tensor core's cut off).
