@@ -1,4 +1,6 @@
-"""GB300-native fused multi-layer RNN operator (LSTM, GRU, tanh RNN).
+"""GB300-native fused multi-layer RNN operator (LSTM, GRU, tanh RNN), with the
+operators of a recurrent language model's other half (``binding.Ops``): a gated
+linear recurrence, a gated feed-forward and products with 4-bit weights.
 
 The compute path lives in ``liblayer_rnn.so`` (hand-written CUDA for sm_103a
 behind a C ABI, declared in ``include/layer_rnn.h``).  ``layer_rnn_gb300.binding``
