@@ -485,12 +485,13 @@ rnn_status_t rnn_glu_backward(rnn_ops_t h, void* stream, int64_t M, int64_t K, i
  * ignored); scales [R, ceil(K / group)] of the handle's type; zeros the same
  * shape, bytes 0..15, or NULL = 8 everywhere.  group: 32, 64 or 128; any K up
  * to 65536 (the last group may be short); ldq (0: ceil(K / 2) rounded up to 16)
- * at least ceil(K / 2) and a multiple of 16.  Meant for few tokens: 16 of them a
- * pass over the weights.
+ * at least ceil(K / 2), a multiple of 16 and at most 2^22.  Meant for few tokens:
+ * 16 of them a pass over the weights.
  * Every group is summed in float32 before its scale.  A token with a value that
  * is not finite has results that are not finite.
  * Errors: RNN_ERR_INVALID_ARG, RNN_ERR_MISALIGNED (bases; scales need 4 or 2
- * bytes, zeros 1), RNN_ERR_UNSUPPORTED (K > 65536, M, R of 2^31 and more). */
+ * bytes, zeros 1), RNN_ERR_UNSUPPORTED (K > 65536, ldq > 2^22, M of 2^31 and
+ * more, R of 2^31 - 1024 and more). */
 rnn_status_t rnn_w4_matvec(rnn_ops_t h, void* stream, int64_t M, int64_t R, int64_t K, int group,
                            const void* x, const uint8_t* q, int64_t ldq, const void* scales,
                            const uint8_t* zeros, void* y);

@@ -101,10 +101,11 @@ rnn_status_t w4_args(const rnn_ops* h, int64_t M, int64_t R, int64_t K, int grou
                      int64_t ldq, const void* scales, const uint8_t* zeros, W4Args* a) {
   if (!h || M < 1 || R < 1 || K < 1 || (group != 32 && group != 64 && group != 128) || !q || !scales)
     return RNN_ERR_INVALID_ARG;
-  if (M >= kLimit || R >= kLimit || K > 65536) return RNN_ERR_UNSUPPORTED;
+  if (M >= kLimit || R >= kLimit - 1024 || K > 65536) return RNN_ERR_UNSUPPORTED;
   const int64_t row = (K + 1) / 2;
   if (ldq == 0) ldq = (row + 15) / 16 * 16;
   if (ldq < row || ldq % 16 != 0) return RNN_ERR_INVALID_ARG;
+  if (ldq > (int64_t(1) << 22)) return RNN_ERR_UNSUPPORTED;  // a block's rows lie within 4 GB
   const bool bf = h->dtype == RNN_BF16;
   if (!on16(q) || reinterpret_cast<uintptr_t>(scales) % (bf ? 2 : 4)) return RNN_ERR_MISALIGNED;
   a->M = M; a->R = R; a->K = K; a->ldq = ldq;

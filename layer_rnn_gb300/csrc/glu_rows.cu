@@ -80,9 +80,11 @@ __device__ __forceinline__ unsigned cl_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cl_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cl_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cl_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_rank0(float2* local, float a, float b) {
   unsigned addr;
@@ -98,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int along = warp % kAlong, beside = warp / kAlong;
   const unsigned csize = cl_size(), rank = cl_rank();
+  if (csize > 1) cl_arrive();  // every block runs before the first is written to
   const int s0 = (int)((int64_t)rank * p.steps / csize), s1 = (int)((int64_t)(rank + 1) * p.steps / csize);
   const int first = s0 + along, steps = first < s1 ? (s1 - first + kAlong - 1) / kAlong : 0;
   const int f0 = (int)(blockIdx.x / csize) * kFeatures, f = min(f0 + beside * 8 + g, p.F - 1);
@@ -198,6 +201,7 @@ __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
       red[(along * kCols + nt * 8 + 2 * t + u) * kFeatures + beside * 8 + g] =
           make_float2(acc[nt][u], acc[nt][2 + u]);
   __syncthreads();
+  if (csize > 1) cl_wait();
   auto put = [&](int i, float gv, float uv) {
     const int fi = f0 + i % kFeatures;
     if (fi >= p.F) return;
@@ -220,7 +224,8 @@ __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
   }
   if (csize > 1) {
     __syncwarp();
-    cl_sync();
+    cl_arrive();
+    cl_wait();
     if (rank == 0)
       for (int i = threadIdx.x; i < part; i += kThreads) {
         float gv = 0.f, uv = 0.f;

@@ -30,7 +30,9 @@
 // The four warps of a block take different rows, or, where the rows alone do not
 // fill the card, the same rows and different parts of K; blocks of a cluster
 // split K where it would not, or where x would not fit.  Partial sums are
-// joined in a fixed order.
+// joined in a fixed order.  For 5 to 16 tokens making the columns takes as long as
+// two row tiles of the product, so eight warps share them and take several row
+// tiles each (16384 x 6007, 8 float32 tokens: 40.0 us with one tile, 35.6 with two).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -54,6 +56,7 @@ struct W4P {
   const uint8_t* zeros;
   void* y;
   int x_bytes;                         // shared memory of the columns
+  int turns;                           // row tiles that each warp takes in turn
 };
 
 __device__ __forceinline__ uint32_t smem_at(const void* p) {
@@ -71,16 +74,16 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// q - z of the eight nibbles of w as fp16 pairs (k0, k4), (k1, k5), (k2, k6),
-// (k3, k7).  A nibble under the exponent of 1024 is 1024 + q; there is room for
-// the second nibble of a byte in place, 1024 + 16 q, of which a sixteenth less
-// (64 + z) is q - z.  z1024, z64: 1024 + z and -(64 + z) in both halves.
 // (w & mask) | bits as one instruction; written as two operators it became two
 __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(bits));
   return r;
 }
+// q - z of the eight nibbles of w as fp16 pairs (k0, k4), (k1, k5), (k2, k6),
+// (k3, k7).  A nibble under the exponent of 1024 is 1024 + q; there is room for
+// the second nibble of a byte in place, 1024 + 16 q, of which a sixteenth less
+// (64 + z) is q - z.  z1024, z64: 1024 + z and -(64 + z) in both halves.
 __device__ __forceinline__ void decode(uint32_t w, __half2 z1024, __half2 z64, uint32_t (&a)[4]) {
   const __half2 s = __float2half2_rn(0.0625f);
 #pragma unroll
@@ -104,9 +107,11 @@ __device__ __forceinline__ unsigned cl_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cl_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cl_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cl_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_rank0(float* local, float v) {
   unsigned a;
@@ -198,18 +203,19 @@ __device__ __forceinline__ void make_columns(const Four& x, int m, unsigned char
 // tiles of 8; MT: row tiles of 16 a warp; kWarps of a block; WK: of them, those
 // that split K (1 or all); GS: 32-weight chunks a group.
 template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
-__global__ void __launch_bounds__(32 * kWarps) w4_kernel(const W4P p) {
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P p) {
   extern __shared__ __align__(128) unsigned char smem[];
   constexpr int kThreads = 32 * kWarps;
   constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
   constexpr int D = MT == 1 ? 4 : 3;         // steps whose loads are under way
-  constexpr bool kDirect = GS == 4;
+  constexpr bool kDirect = GS == 4, kTurns = kWarps == 8;
   constexpr int kTok = F32 ? 1 : 2;          // tokens of a lane and column tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const unsigned csize = cl_size(), rank = cl_rank();
+  if (csize > 1) cl_arrive();  // every block runs before the first is written to
   const int cols = F32 ? 2 * p.toks : p.toks;
-  const int block0 = (int)(blockIdx.x / csize) * kBlockRows;
-  const int row0 = block0 + (WK == 1 ? warp * kRows : 0);
+  const int turns = kTurns ? p.turns : 1, rows_all = kBlockRows * turns;  // of the block
+  const int block0 = (int)(blockIdx.x / csize) * rows_all;
   const int kb0 = (int)((int64_t)rank * p.nkb / csize), kb1 = (int)((int64_t)(rank + 1) * p.nkb / csize);
   const int first = kb0 + (WK == 1 ? 0 : warp);
   const int steps = first < kb1 ? (kb1 - first + WK - 1) / WK : 0;
@@ -223,14 +229,18 @@ __global__ void __launch_bounds__(32 * kWarps) w4_kernel(const W4P p) {
   const char* sbase = static_cast<const char*>(p.scales) + (int64_t)block0 * p.groups * (F32 ? 4 : 2);
   const uint8_t* zbase = p.zeros + (int64_t)block0 * p.groups;
   uint32_t wo[MT][2], so[MT][2];
+  auto set_rows = [&](int turn) {
+    const int row0 = block0 + turn * kBlockRows + (WK == 1 ? warp * kRows : 0);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t row = (uint32_t)(min(row0 + mt * 16 + h * 8 + g, p.R - 1) - block0);
-      wo[mt][h] = row * (uint32_t)p.ldq;
-      so[mt][h] = row * (uint32_t)p.groups;
-    }
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t row = (uint32_t)(min(row0 + mt * 16 + h * 8 + g, p.R - 1) - block0);
+        wo[mt][h] = row * (uint32_t)p.ldq;
+        so[mt][h] = row * (uint32_t)p.groups;
+      }
+  };
+  set_rows(0);
   uint4 w[D][MT][2];
   uint32_t sc[D][MT][2], zp[ZERO ? D : 1][MT][2];
   auto fetch = [&](int slot, int i) {
@@ -253,122 +263,30 @@ __global__ void __launch_bounds__(32 * kWarps) w4_kernel(const W4P p) {
 #pragma unroll
   for (int i = 0; i < D; ++i) fetch(i, i);
 
-  // x: eight loads of a warp under way at a time
+  // x: eight loads of a warp under way at a time, pair e of (block, token)
   constexpr int kBatch = 8;
-  const int pairs = (kb1 - kb0) * p.toks;
-  for (int e0 = warp; e0 < pairs; e0 += kBatch * kWarps) {
+  const int nb = kb1 - kb0, db = kWarps / p.toks, dm = kWarps - db * p.toks;
+  int b = warp / p.toks, m = warp - b * p.toks;
+  while (b < nb) {
     Four x[kBatch];
+    int bj = b, mj = m;
+    auto next = [&](int& b, int& m) {
+      b += db;
+      m += dm;
+      if (m >= p.toks) { m -= p.toks; ++b; }
+    };
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int e = min(e0 + j * kWarps, pairs - 1);
-      x[j] = get_four<F32>(p, kb0 + e / p.toks, e % p.toks);
+      if (bj < nb) x[j] = get_four<F32>(p, kb0 + bj, mj);
+      next(bj, mj);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int e = e0 + j * kWarps;
-      if (e >= pairs) break;
-      const int b = e / p.toks, m = e - b * p.toks;
-      make_columns<F32, kDirect>(x[j], m, smem + b * (cols * 256), cols, muls + b * kTokens + m);
+      if (b < nb) make_columns<F32, kDirect>(x[j], m, smem + b * (cols * 256), cols, muls + b * kTokens + m);
+      next(b, m);
     }
   }
   __syncthreads();
-
-  float fin[MT][NT][2 * kTok];  // rows g and g + 8
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2 * kTok; ++i) fin[mt][nt][i] = 0.f;
-
-  const unsigned char* xa[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-    xa[nt] = smem + (first - kb0) * (cols * 256) + ((nt * 8 + g < cols ? nt * 8 + g : 0) * 4 + t) * 16;
-  const int x_chunk = cols * 64;
-  const float* ma = muls + (first - kb0) * kTokens + kTok * t;
-  for (int i0 = 0; i0 < steps; i0 += D) {
-#pragma unroll
-    for (int slot = 0; slot < D; ++slot) {
-      if (i0 + slot >= steps) break;
-      uint32_t a[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 v = w[slot][mt][h];
-          a[mt][h][0] = v.x; a[mt][h][1] = v.y; a[mt][h][2] = v.z; a[mt][h][3] = v.w;
-          if (!kDirect) transpose_quad(a[mt][h], t);
-        }
-      uint32_t zz[MT][2];  // 1024 + z in both halves, of this lane's group
-      if (ZERO)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) zz[mt][h] = 0x64006400u | zp[ZERO ? slot : 0][mt][h] * 0x10001u;
-      float mul[NT][kTok];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int u = 0; u < kTok; ++u) mul[nt][u] = ma[nt * 4 * kTok + u];
-      float acc[MT][NT][4], s[MT][2];
-      __half2 z1024[MT][2], z64[MT][2];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c % GS == 0) {
-          const int src = (lane & 28) | (c / GS);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v = sc[slot][mt][h], z = 0x64086408u;
-              if (ZERO) z = zz[mt][h];
-              if (GS < 4) {
-                v = __shfl_sync(0xffffffffu, v, src);
-                if (ZERO) z = __shfl_sync(0xffffffffu, z, src);
-              }
-              s[mt][h] = __uint_as_float(F32 ? v : v << 16);
-              z1024[mt][h] = *reinterpret_cast<const __half2*>(&z);
-              z64[mt][h] = __hsub2(__float2half2_rn(960.f), z1024[mt][h]);
-            }
-        }
-        uint4 b[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          b[nt] = *reinterpret_cast<const uint4*>(xa[nt] + c * x_chunk);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t u[4], d[4];
-          decode(a[mt][0][c], z1024[mt][0], z64[mt][0], u);
-          decode(a[mt][1][c], z1024[mt][1], z64[mt][1], d);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(acc[mt][nt], u[0], d[0], u[1], d[1], b[nt].x, b[nt].y, c % GS == 0);
-            mma(acc[mt][nt], u[2], d[2], u[3], d[3], b[nt].z, b[nt].w, false);
-          }
-        }
-        if (c % GS == GS - 1) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                  const float v = F32 ? fmaf(acc[mt][nt][2 * h + 1], 0x1p-11f, acc[mt][nt][2 * h])
-                                      : acc[mt][nt][2 * h + k];
-                  fin[mt][nt][h * kTok + k] =
-                      fmaf(s[mt][h] * mul[nt][k], v, fin[mt][nt][h * kTok + k]);
-                }
-        }
-      }
-      fetch(slot, i0 + slot + D);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) xa[nt] += WK * 4 * x_chunk;
-      ma += WK * kTokens;
-    }
-  }
 
   auto put = [&](int row, int m, float v) {
     if (row >= p.R) return;
@@ -379,41 +297,155 @@ __global__ void __launch_bounds__(32 * kWarps) w4_kernel(const W4P p) {
   // joined sums: [block or warp][token][row].  Blocks of a cluster write theirs
   // to block 0; warps that split K to their own block.
   float* across = muls + (p.nkb + (int)csize - 1) / (int)csize * kTokens;
-  const int part = p.toks * kBlockRows;
-  float* within = across + (csize > 1 ? csize * part : 0);
+  const int share = p.toks * rows_all;
+  float* within = across + (csize > 1 ? csize * share : 0);
+  float fin[MT][NT][2 * kTok];  // rows g and g + 8
+  for (int turn = 0; turn < turns; ++turn) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2 * kTok; ++i) fin[mt][nt][i] = 0.f;
+    const unsigned char* xa[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
+      xa[nt] = smem + (first - kb0) * (cols * 256) + ((nt * 8 + g < cols ? nt * 8 + g : 0) * 4 + t) * 16;
+    const int x_chunk = cols * 64;
+    const float* ma = muls + (first - kb0) * kTokens + kTok * t;
+    for (int i0 = 0; i0 < steps; i0 += D) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int slot = 0; slot < D; ++slot) {
+        if (i0 + slot >= steps) break;
+        uint32_t a[MT][2][4];
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-          const int m = (nt * 4 + t) * kTok + k, r = (WK == 1 ? warp * kRows : 0) + mt * 16 + h * 8 + g;
-          const float v = fin[mt][nt][h * kTok + k];
-          if (m >= p.toks) continue;
-          if (WK > 1) within[warp * part + m * kBlockRows + r] = v;
-          else if (csize > 1) st_rank0(across + (int)rank * part + m * kBlockRows + r, v);
-          else put(block0 + r, m, v);
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = w[slot][mt][h];
+            a[mt][h][0] = v.x; a[mt][h][1] = v.y; a[mt][h][2] = v.z; a[mt][h][3] = v.w;
+            if (!kDirect) transpose_quad(a[mt][h], t);
+          }
+        uint32_t zz[MT][2];  // 1024 + z in both halves, of this lane's group
+        if (ZERO)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) zz[mt][h] = 0x64006400u | zp[ZERO ? slot : 0][mt][h] * 0x10001u;
+        float mul[NT][kTok];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int u = 0; u < kTok; ++u) mul[nt][u] = ma[nt * 4 * kTok + u];
+        float acc[MT][NT][4], s[MT][2], part[MT][NT][2 * kTok];  // part: without the tokens' scale
+        __half2 z1024[MT][2], z64[MT][2];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c % GS == 0) {
+            const int src = (lane & 28) | (c / GS);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t v = sc[slot][mt][h], z = 0x64086408u;
+                if (ZERO) z = zz[mt][h];
+                if (GS < 4) {
+                  v = __shfl_sync(0xffffffffu, v, src);
+                  if (ZERO) z = __shfl_sync(0xffffffffu, z, src);
+                }
+                s[mt][h] = __uint_as_float(F32 ? v : v << 16);
+                z1024[mt][h] = *reinterpret_cast<const __half2*>(&z);
+                z64[mt][h] = __hsub2(__float2half2_rn(960.f), z1024[mt][h]);
+              }
+          }
+          uint4 b[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            b[nt] = *reinterpret_cast<const uint4*>(xa[nt] + c * x_chunk);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t u[4], d[4];
+            decode(a[mt][0][c], z1024[mt][0], z64[mt][0], u);
+            decode(a[mt][1][c], z1024[mt][1], z64[mt][1], d);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(acc[mt][nt], u[0], d[0], u[1], d[1], b[nt].x, b[nt].y, c % GS == 0);
+              mma(acc[mt][nt], u[2], d[2], u[3], d[3], b[nt].z, b[nt].w, false);
+            }
+          }
+          if (c % GS == GS - 1) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int k = 0; k < kTok; ++k) {
+                    const float v = F32 ? fmaf(acc[mt][nt][2 * h + 1], 0x1p-11f, acc[mt][nt][2 * h])
+                                        : acc[mt][nt][2 * h + k];
+                    float& sum = part[mt][nt][h * kTok + k];
+                    sum = c < GS ? s[mt][h] * v : fmaf(s[mt][h], v, sum);
+                  }
+          }
         }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2 * kTok; ++i)
+              fin[mt][nt][i] = fmaf(mul[nt][i % kTok], part[mt][nt][i], fin[mt][nt][i]);
+        fetch(slot, i0 + slot + D);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xa[nt] += WK * 4 * x_chunk;
+        ma += WK * kTokens;
+      }
+    }
+
+    __syncwarp();
+    if (csize > 1 && turn == 0) cl_wait();
+    if (turn + 1 < turns) {
+      set_rows(turn + 1);
+#pragma unroll
+      for (int i = 0; i < D; ++i) fetch(i, i);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < kTok; ++k) {
+            const int m = (nt * 4 + t) * kTok + k;
+            const int r = turn * kBlockRows + (WK == 1 ? warp * kRows : 0) + mt * 16 + h * 8 + g;
+            const float v = fin[mt][nt][h * kTok + k];
+            if (m >= p.toks) continue;
+            if (WK > 1) within[warp * share + m * rows_all + r] = v;
+            else if (csize > 1) st_rank0(across + (int)rank * share + m * rows_all + r, v);
+            else put(block0 + r, m, v);
+          }
+  }
   if (WK > 1) {
     __syncthreads();
-    for (int i = threadIdx.x; i < part; i += kThreads) {
+    for (int i = threadIdx.x; i < share; i += kThreads) {
       float v = 0.f;
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u) v += within[u * part + i];
-      if (csize > 1) st_rank0(across + (int)rank * part + i, v);
-      else put(block0 + i % kBlockRows, i / kBlockRows, v);
+      for (int u = 0; u < kWarps; ++u) v += within[u * share + i];
+      if (csize > 1) st_rank0(across + (int)rank * share + i, v);
+      else put(block0 + i % rows_all, i / rows_all, v);
     }
   }
   if (csize > 1) {
     __syncwarp();
-    cl_sync();
+    cl_arrive();
+    cl_wait();
     if (rank == 0)
-      for (int i = threadIdx.x; i < part; i += kThreads) {
+      for (int i = threadIdx.x; i < share; i += kThreads) {
         float v = 0.f;
-        for (unsigned c = 0; c < csize; ++c) v += across[c * part + i];
-        put(block0 + i % kBlockRows, i / kBlockRows, v);
+        for (unsigned c = 0; c < csize; ++c) v += across[c * share + i];
+        put(block0 + i % rows_all, i / rows_all, v);
       }
   }
 }
@@ -422,7 +454,7 @@ template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
 cudaError_t launch(W4P p, const W4Args& a, cudaStream_t st) {
   auto kernel = w4_kernel<F32, NT, MT, kWarps, WK, GS, ZERO>;
   constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
-  const int blocks = (p.R + kBlockRows - 1) / kBlockRows;
+  int blocks = (p.R + kBlockRows - 1) / kBlockRows;
   // K over the blocks of a cluster: until x fits, and until the card has two
   // blocks an SM as long as each warp keeps four steps
   const int cols = p.toks * (F32 ? 2 : 1);
@@ -430,9 +462,16 @@ cudaError_t launch(W4P p, const W4Args& a, cudaStream_t st) {
   int c = 1;
   while (c < 8 && x_of(c) > (kWarps == 8 ? kXBytes : kXBytes / 2)) c *= 2;
   while (c < 8 && blocks * c < 2 * a.num_sms && p.nkb >= 8 * c * WK) c *= 2;
+  // eight warps a block are two blocks an SM: more than they hold at once take up to
+  // four row tiles a warp, for columns that are made once
+  p.turns = 1;
+  if (kWarps == 8) {
+    p.turns = std::max(1, std::min(4, (blocks * c + 2 * a.num_sms - 1) / (2 * a.num_sms)));
+    blocks = (blocks + p.turns - 1) / p.turns;
+  }
   p.x_bytes = x_of(c);
   const size_t smem = (size_t)p.x_bytes + (p.nkb + c - 1) / c * kTokens * 4 +
-                      (size_t)((c > 1 ? c : 0) + (WK > 1 ? kWarps : 0)) * p.toks * kBlockRows * 4;
+                      (size_t)((c > 1 ? c : 0) + (WK > 1 ? kWarps : 0)) * p.toks * kBlockRows * p.turns * 4;
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);

@@ -76,6 +76,14 @@ def test_split_over_a_cluster(M, R, K, group, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,R,K,group", [(12, 40001, 130, 32), (16, 100003, 97, 64), (9, 12001, 4100, 128),
+                                         (6, 50001, 260, 32)])
+def test_more_rows_than_the_card_holds_at_once(M, R, K, group, dtype):
+    d = make(M, R, K, group, True, dtype, 11)
+    assert harness.rel_err(run(d, group, dtype), want(d, group)) <= bar(dtype, K)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_wider_pitch_and_garbage_past_the_row(dtype):
     d = make(3, 40, 333, 64, True, dtype, 1, pitch=512)
     a = run(d, 64, dtype)

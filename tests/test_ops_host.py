@@ -100,6 +100,13 @@ def test_w4_refuses(L, h):
     assert quant(W=None) == INVALID and quant(group=8) == INVALID and quant(W=ODD) == MISALIGNED
 
 
+def test_w4_refuses_pitches_beyond_its_offsets(L, h):
+    call = lambda R, ldq: L.rnn_w4_matvec(h, None, 1, R, 64, 32, P, P, ldq, P, None, P)  # noqa: E731
+    assert call(4, (1 << 22) + 16) == UNSUPPORTED and call(4, 1 << 40) == UNSUPPORTED
+    assert call((1 << 31) - 1024, 0) == UNSUPPORTED
+    assert L.rnn_w4_quantize(h, None, 4, 64, 32, P, P, (1 << 22) + 16, P, None) == UNSUPPORTED
+
+
 def test_glu_workspace_and_refusals(L, h):
     b = ctypes.c_int64()
     size = lambda M, K, F, bwd: (L.rnn_glu_workspace_size(h, M, K, F, bwd, ctypes.byref(b)), b.value)  # noqa: E731
