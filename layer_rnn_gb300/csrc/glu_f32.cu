@@ -51,6 +51,12 @@ __device__ __forceinline__ float unscale(unsigned mb) {
   return __int_as_float((127 - s) << 23);
 }
 
+// of a finite value, as bits; others have none
+__device__ __forceinline__ unsigned magnitude(float v) {
+  const unsigned b = __float_as_uint(v) & 0x7fffffffu;
+  return b < 0x7f800000u ? b : 0u;
+}
+
 template <int PROD, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     glu_f32_kernel(const __grid_constant__ Maps maps, const __grid_constant__ P p) {
@@ -236,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             : "memory");
       }
     };
-    unsigned mx = 0;
+    float mx = 0.f;
     int blk = 0, n = 0;
     bool ok = true;
     while (ok && walk_next(p, w, pair, pairs)) {
@@ -326,6 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
               dy_ph ^= 1u;
             }
+            float most = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -347,9 +354,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 value_slope(s0[i], ACT, v, d);
                 s0[i] = y[u] * s1[i] * d;
                 s1[i] = y[u] * v;
-                mx = max(mx, max(__float_as_uint(s0[i]) & 0x7fffffffu, __float_as_uint(s1[i]) & 0x7fffffffu));
+                most = fmaxf(most, fmaxf(fabsf(s0[i]), fabsf(s1[i])));
               }
             }
+            // NaN does not enter; a run with an infinity, whose row of dx is lost, neither
+            if (most < __int_as_float(0x7f800000)) mx = fmaxf(mx, most);
           }
           if (PROD == kForward || !p.tma_dy) box_free();
           __syncwarp();
@@ -365,8 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (PROD == kDgu) {
       __syncwarp();
-      mx = __reduce_max_sync(0xffffffffu, mx);
-      if (lane == 0) atomicMax(p.omax, mx);
+      const unsigned most = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+      if (lane == 0) atomicMax(p.omax, most);
     }
   }
   __syncwarp();
@@ -440,22 +449,114 @@ bool map_f32(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_
   return tma_encode(m, 3, false, ptr, dims, strides, box);
 }
 
-// src [rows][cols], row pitch lds, to pairs, with the scale of *mx
-cudaError_t split(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& q,
-                  const unsigned* mx, cudaStream_t st) {
-  return split_f16_operand(src, rows, cols, lds, q.hi, q.lo, q.ld, false, mx, st);
+// Two dense operands at most to pairs: their largest finite magnitudes, then the
+// pairs, one launch each, bound by memory (x and W of 6000 x 800 x 2160: 9 and 12
+// us; a launch for each operand 30 in all).  A value that is not finite sets no
+// scale, so it spoils only the results that it enters.
+struct Job {
+  const float* src;
+  __half* hi;
+  __half* lo;
+  unsigned* mx;
+  int64_t rows, cols, lds, ld;  // lds: the source's pitch; ld: the pairs', a multiple of 8
+};
+struct Jobs { Job j[2]; };
+
+// sources without gaps (lds = cols), on 16 bytes
+__global__ void __launch_bounds__(256) largest_kernel(const Jobs jobs) {
+  __shared__ unsigned red[2][8];
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t n = jobs.j[k].rows * jobs.j[k].cols;
+    const float4* v = reinterpret_cast<const float4*>(jobs.j[k].src);
+    unsigned m = 0;
+#pragma unroll 4
+    for (int64_t i = first; i < n / 4; i += all) {
+      const float4 q = __ldg(v + i);
+      m = max(max(m, max(magnitude(q.x), magnitude(q.y))), max(magnitude(q.z), magnitude(q.w)));
+    }
+    if (first < n % 4) m = max(m, magnitude(__ldg(jobs.j[k].src + (n - n % 4) + first)));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = m;
+  }
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    unsigned m = 0;
+    for (int w = 0; w < 8; ++w) m = max(m, red[threadIdx.x][w]);
+    if (m) atomicMax(threadIdx.x ? jobs.j[1].mx : jobs.j[0].mx, m);
+  }
+}
+
+// a thread takes 8 columns of a row
+__global__ void __launch_bounds__(256) pairs_kernel(const Jobs jobs) {
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const Job& q = jobs.j[k];
+    const int64_t n = q.rows * q.ld / 8;
+    if (n == 0) continue;
+    const float s = 1.0f / unscale(*q.mx);
+    const bool flat = q.lds == q.ld;  // columns past the last are copied along, and never read
+#pragma unroll 2
+    for (int64_t i = first; i < n; i += all) {
+      float v[8];
+      if (flat) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(q.src) + 2 * i),
+                     b = __ldg(reinterpret_cast<const float4*>(q.src) + 2 * i + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      } else {
+        const int64_t r = i / (q.ld / 8), c = (i - r * (q.ld / 8)) * 8;
+        const float* row = q.src + r * q.lds;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = c + u < q.cols ? __ldg(row + c + u) : 0.f;
+      }
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float x = v[2 * u] * s, y = v[2 * u + 1] * s;  // exact
+        const __half2 a = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(a);
+        const __half2 b = __floats2half2_rn(x - f.x, y - f.y);
+        h[u] = *reinterpret_cast<const uint32_t*>(&a);
+        l[u] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      reinterpret_cast<uint4*>(q.hi)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+      reinterpret_cast<uint4*>(q.lo)[i] = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+  }
+}
+
+Job job(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& q, unsigned* mx) {
+  Job j;
+  j.src = src;
+  j.hi = reinterpret_cast<__half*>(q.hi);
+  j.lo = reinterpret_cast<__half*>(q.lo);
+  j.mx = mx;
+  j.rows = rows; j.cols = cols; j.lds = lds; j.ld = q.ld;
+  return j;
+}
+cudaError_t make_pairs(const Jobs& jobs, int num_sms, cudaStream_t st) {
+  const int64_t n = std::max(jobs.j[0].rows * jobs.j[0].ld, jobs.j[1].rows * jobs.j[1].ld) / 8;
+  const int64_t blocks = std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 16);
+  pairs_kernel<<<(unsigned)blocks, 256, 0, st>>>(jobs);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return cudaGetLastError();
 }
 
 // x and W as pairs; mx[0], mx[1] their largest magnitudes
 cudaError_t operands(const GluArgs& a, unsigned* mx, const Pairs& x, const Pairs& w,
                      cudaStream_t st) {
-  const float* xf = static_cast<const float*>(a.x);
-  const float* wf = static_cast<const float*>(a.W);
+  Jobs jobs = {{job(static_cast<const float*>(a.x), a.M, a.K, a.K, x, mx),
+                job(static_cast<const float*>(a.W), 2 * a.F, a.K, a.K, w, mx + 1)}};
   TRY(cudaMemsetAsync(mx, 0, 256, st));
-  TRY(absmax_operand(xf, a.M, a.K, a.K, mx, a.num_sms, st));
-  TRY(absmax_operand(wf, 2 * a.F, a.K, a.K, mx + 1, a.num_sms, st));
-  TRY(split(xf, a.M, a.K, a.K, x, mx, st));
-  return split(wf, 2 * a.F, a.K, a.K, w, mx + 1, st);
+  const int64_t n = std::max(a.M, 2 * a.F) * a.K;
+  const int64_t blocks = std::min<int64_t>((n + 4095) / 4096, (int64_t)a.num_sms * 6);
+  largest_kernel<<<(unsigned)blocks, 256, 0, st>>>(jobs);
+  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  TRY(cudaGetLastError());
+  return make_pairs(jobs, a.num_sms, st);
 }
 
 bool gated_maps(const GluArgs& a, const Pairs& x, const Pairs& w, Maps* m) {
@@ -518,7 +619,8 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.omax = mx + 2;
     TRY(launch<kDgu>(maps, p, a, st));
   }
-  TRY(split(dgu, 2 * a.M, a.F, Fp, d, mx + 2, st));
+  Jobs jobs = {{job(dgu, 2 * a.M, a.F, Fp, d, mx + 2), job(nullptr, 0, 0, 0, d, mx + 3)}};
+  TRY(make_pairs(jobs, a.num_sms, st));
   P p = {};
   p.n_tiles = (int)ceil_div(a.K, kCols);
   p.cols = (int)a.K;

@@ -64,10 +64,10 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// v = hi + lo, hi its nearest value with 11 significant bits (NaN and infinities
-// stay in hi)
+// v = hi + lo, hi its nearest value with 11 significant bits.  A v that is not
+// finite makes lo NaN and so every result that it enters.
 __device__ __forceinline__ void split(uint32_t v, uint32_t& hi, uint32_t& lo) {
-  hi = (v & 0x7f800000u) == 0x7f800000u ? v : (v + 0x1000u) & 0xffffe000u;
+  hi = (v + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(__uint_as_float(v) - __uint_as_float(hi));
 }
 __device__ __forceinline__ unsigned cl_size() {

@@ -152,3 +152,27 @@ def test_gradient_against_differences():
                 loss(dict(d, x=d["x"] - e * v, W=d["W"] - e * w))) / (2 * e)
         want = (out["dx"] * v).sum() + (out["dW"] * w).sum()
         assert abs(diff - want) < 2e-2 * max(1.0, abs(want))
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,K,F", [(150, 72, 24), (300, 136, 200), (130, 37, 41)])
+def test_many_rows_keep_a_value_that_is_not_finite_apart(M, K, F, dtype, value):
+    """A token's rows of y and dx take its value that is not finite, no others do;
+    a weight's feature likewise."""
+    d = make(M, K, F, dtype)
+    good = run(d, "silu", dtype)
+    x, W = d["x"], d["W"]
+    d["x"] = x.copy()
+    d["x"][3, 5] = value
+    bad = run(d, "silu", dtype)
+    keep = np.arange(M) != 3
+    # float32: without that value the operand's scale, and so its last bits, may be others
+    same = lambda a, b: np.isfinite(a).all() and harness.rel_err(a, b) <= (1e-6 if dtype == "f32" else 0)  # noqa: E731
+    assert not np.isfinite(bad["y"][3]).any()
+    assert same(bad["y"][keep], good["y"][keep]) and same(bad["dx"][keep], good["dx"][keep])
+    d["x"], d["W"] = x, W.copy()
+    d["W"][7, 2] = value
+    bad = run(d, "silu", dtype, backward=False)
+    keep = np.arange(F) != 7
+    assert same(bad["y"][:, keep], good["y"][:, keep])
