@@ -102,6 +102,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cl_sync();
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
+  next_may_start();
+  wait_for_last();
 
   Walk w;
   walk_start(p, w, pair, pairs);
@@ -379,29 +381,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Rows of `cols` bf16 of two matrices to rows of pitch ldd (a multiple of 8), so
-// that TMA can read them.  A thread makes 16 bytes from five aligned words: a
-// row of an odd number of values starts in the middle of a word.
+// that TMA can read them.  A thread makes 16 bytes from the two aligned 16-byte
+// pieces of the source that hold them (of the last piece what is past the matrix
+// is loaded and dropped).  I: wide enough to count the results; the division by the
+// pieces of a row took half the time in 64 bits.
 struct PadP {
-  const uint32_t* src[2];
+  const uint4* src[2];
   uint4* dst[2];
   int64_t rows[2];
   int cols, ldd;
 };
+template <typename I>
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadP p) {
-  const int per = p.ldd / 8;
-  const int64_t n0 = p.rows[0] * per, total = n0 + p.rows[1] * per;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  next_may_start();
+  const I per = (I)(p.ldd / 8), n0 = (I)p.rows[0] * per, total = n0 + (I)p.rows[1] * per;
+  for (I i = (I)blockIdx.x * 256 + threadIdx.x; i < total; i += (I)gridDim.x * 256) {
     const int m = i >= n0;
-    const int64_t e = m ? i - n0 : i, r = e / per;
+    const I e = m ? i - n0 : i, r = e / per;
     const int c = (int)(e - r * per) * 8;
-    const int64_t at = r * p.cols + c, last = (p.rows[m] * p.cols - 1) >> 1;  // last word
-    uint32_t w[5];
+    const int64_t at = (int64_t)r * p.cols + c, last = (p.rows[m] * p.cols - 1) >> 3;
+    const uint4 q0 = __ldg(p.src[m] + (at >> 3)), q1 = __ldg(p.src[m] + min((at >> 3) + 1, last));
+    const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    const int skip = (int)(at & 7);  // values of the first piece before the row's
+    uint32_t v[6], u[5], o[4];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = __ldcs(p.src[m] + min((at >> 1) + k, last));
-    uint32_t o[4];
+    for (int k = 0; k < 6; ++k) v[k] = skip & 4 ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) u[k] = skip & 2 ? v[k + 1] : v[k];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      o[k] = at & 1 ? __funnelshift_r(w[k], w[k + 1], 16) : w[k];
+      o[k] = skip & 1 ? __funnelshift_r(u[k], u[k + 1], 16) : u[k];
       if (c + 2 * k >= p.cols) o[k] = 0;
       else if (c + 2 * k + 1 >= p.cols) o[k] &= 0xffffu;
     }
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadP p) {
 }
 
 template <int PROD, int ACT>
-cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, bool after, cudaStream_t st) {
   auto kernel = glu_gemm_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
@@ -418,20 +427,18 @@ cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st)
   // few row tiles walked together keep their rows of A in L2 beside all of B
   p.group = std::min(p.m_tiles, 16);
   p.status = a.status;
-  kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  e = cudaGetLastError();
+  e = launch_kernel(after, kernel, 2 * pairs, kThreads, kSmem, st, maps, p);
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
   return launch_join<bf16, kTile>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
-cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, bool after, cudaStream_t st) {
   if constexpr (PROD == kForward || PROD == kDgu) {
-    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
-    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, after, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, after, st);
   }
-  return launch_act<PROD, 2>(maps, p, a, st);
+  return launch_act<PROD, 2>(maps, p, a, after, st);
 }
 
 // x and W with rows that TMA can read: as they are, or copied
@@ -440,7 +447,7 @@ struct Operands {
   const void* W;
   int64_t ld;
 };
-cudaError_t operands(const GluArgs& a, char** ws, Operands* o, bool copy, cudaStream_t st) {
+cudaError_t operands(const GluArgs& a, char** ws, Operands* o, cudaStream_t st) {
   o->x = a.x; o->W = a.W; o->ld = a.K;
   if (a.K % 8 == 0) return cudaSuccess;
   o->ld = pad8(a.K);
@@ -448,10 +455,9 @@ cudaError_t operands(const GluArgs& a, char** ws, Operands* o, bool copy, cudaSt
   char* wc = xc + round256(a.M * o->ld * 2);
   *ws = wc + round256(2 * a.F * o->ld * 2);
   o->x = xc; o->W = wc;
-  if (!copy) return cudaSuccess;
   PadP p;
-  p.src[0] = static_cast<const uint32_t*>(a.x);
-  p.src[1] = static_cast<const uint32_t*>(a.W);
+  p.src[0] = static_cast<const uint4*>(a.x);
+  p.src[1] = static_cast<const uint4*>(a.W);
   p.dst[0] = reinterpret_cast<uint4*>(xc);
   p.dst[1] = reinterpret_cast<uint4*>(wc);
   p.rows[0] = a.M;
@@ -459,9 +465,9 @@ cudaError_t operands(const GluArgs& a, char** ws, Operands* o, bool copy, cudaSt
   p.cols = (int)a.K;
   p.ldd = (int)o->ld;
   const int64_t work = (a.M + 2 * a.F) * (o->ld / 8);
-  pad_rows_kernel<<<(unsigned)std::min<int64_t>(ceil_div(work, 256), (int64_t)a.num_sms * 16), 256, 0, st>>>(p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError();
+  const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(work, 256), (int64_t)a.num_sms * 16);
+  return work < (int64_t(1) << 31) ? launch_kernel(false, pad_rows_kernel<uint32_t>, blocks, 256, 0, st, p)
+                                   : launch_kernel(false, pad_rows_kernel<int64_t>, blocks, 256, 0, st, p);
 }
 
 }  // namespace
@@ -477,7 +483,7 @@ int64_t glu_tc_workspace(int64_t M, int64_t K, int64_t F, bool backward) {
 cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st) {
   char* ws = static_cast<char*>(a.workspace);
   Operands o;
-  cudaError_t e = operands(a, &ws, &o, true, st);
+  cudaError_t e = operands(a, &ws, &o, st);
   if (e != cudaSuccess) return e;
   Maps maps = {};
   P p = {};
@@ -491,13 +497,13 @@ cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st) {
   p.nkb = (int)ceil_div(a.K, 64);
   p.rows = (int)a.M; p.cols = (int)a.F;
   p.out = a.y; p.ld_out = a.F;
-  return launch<kForward>(maps, p, a, st);
+  return launch<kForward>(maps, p, a, a.K % 8 != 0, st);
 }
 
 cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
   char* ws = static_cast<char*>(a.workspace);
   Operands o;
-  cudaError_t e = operands(a, &ws, &o, true, st);
+  cudaError_t e = operands(a, &ws, &o, st);
   if (e != cudaSuccess) return e;
   const int64_t Fp = pad8(a.F);
   char* dgu = ws;
@@ -517,7 +523,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.nkb = (int)ceil_div(a.K, 64);
     p.rows = (int)a.M; p.cols = (int)a.F;
       p.dy = a.dy; p.ld_dy = a.F;
-    e = launch<kDgu>(maps, p, a, st);
+    e = launch<kDgu>(maps, p, a, a.K % 8 != 0, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dx) {
@@ -535,7 +541,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.rows = (int)a.M; p.cols = (int)a.K;
     p.out = a.dx; p.ld_out = a.K;
     p.part = part;
-    e = launch<kDx>(maps, p, a, st);
+    e = launch<kDx>(maps, p, a, true, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dW) {
@@ -552,7 +558,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.rows = (int)a.F; p.cols = (int)a.K;
     p.out = a.dW; p.ld_out = a.K;
     p.part = part;
-    e = launch<kDw>(maps, p, a, st);
+    e = launch<kDw>(maps, p, a, true, st);
   }
   return e;
 }

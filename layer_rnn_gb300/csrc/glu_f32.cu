@@ -99,6 +99,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cl_sync();
   tc::fence_after();
   const uint32_t tmem = tmem_slot;
+  next_may_start();
+  wait_for_last();
 
   Walk w;
   walk_start(p, w, pair, pairs);
@@ -190,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int e = warp - 2, q = warp & 3, half = e >> 2;
     const int c0 = kGated ? 64 * half : 128 * half, c1 = kGated ? 128 + 64 * half : 128 * half + 64;
     const uint32_t tempty = map_rank(tempty0, 0);
-    const float ia = unscale(*p.amax), ib = unscale(*p.bmax);
+    const float ia = unscale(__ldcg(p.amax)), ib = unscale(__ldcg(p.bmax));
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     // results leave through a box of 32 rows x 32 columns in shared memory (16-byte
     // piece j of row r at piece j ^ (r & 7)): stores by rows of a lane each took as
@@ -388,27 +390,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PROD, int ACT>
-cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, bool after, cudaStream_t st) {
   auto kernel = glu_f32_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = plan_pairs(&p, a.num_sms, 8);  // 256 KB each way, three products a block
   p.group = std::min(p.m_tiles, 16);
   p.status = a.status;
-  kernel<<<2 * pairs, kThreads, kSmem, st>>>(maps, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  e = cudaGetLastError();
+  e = launch_kernel(after, kernel, 2 * pairs, kThreads, kSmem, st, maps, p);
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
   return launch_join<float, kCols>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
-cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, bool after, cudaStream_t st) {
   if constexpr (PROD == kForward || PROD == kDgu) {
-    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
-    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, after, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, after, st);
   }
-  return launch_act<PROD, 2>(maps, p, a, st);
+  return launch_act<PROD, 2>(maps, p, a, after, st);
 }
 
 struct Pairs {
@@ -464,6 +464,7 @@ struct Jobs { Job j[2]; };
 
 // sources without gaps (lds = cols), on 16 bytes
 __global__ void __launch_bounds__(256) largest_kernel(const Jobs jobs) {
+  next_may_start();
   __shared__ unsigned red[2][8];
   const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
 #pragma unroll
@@ -490,27 +491,29 @@ __global__ void __launch_bounds__(256) largest_kernel(const Jobs jobs) {
 
 // a thread takes 8 columns of a row
 __global__ void __launch_bounds__(256) pairs_kernel(const Jobs jobs) {
+  next_may_start();
+  wait_for_last();
   const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const Job& q = jobs.j[k];
     const int64_t n = q.rows * q.ld / 8;
     if (n == 0) continue;
-    const float s = 1.0f / unscale(*q.mx);
+    const float s = 1.0f / unscale(__ldcg(q.mx));
     const bool flat = q.lds == q.ld;  // columns past the last are copied along, and never read
 #pragma unroll 2
     for (int64_t i = first; i < n; i += all) {
       float v[8];
       if (flat) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(q.src) + 2 * i),
-                     b = __ldg(reinterpret_cast<const float4*>(q.src) + 2 * i + 1);
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(q.src) + 2 * i),
+                     b = __ldcs(reinterpret_cast<const float4*>(q.src) + 2 * i + 1);
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
       } else {
         const int64_t r = i / (q.ld / 8), c = (i - r * (q.ld / 8)) * 8;
         const float* row = q.src + r * q.lds;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = c + u < q.cols ? __ldg(row + c + u) : 0.f;
+        for (int u = 0; u < 8; ++u) v[u] = c + u < q.cols ? __ldcs(row + c + u) : 0.f;
       }
       uint32_t h[4], l[4];
 #pragma unroll
@@ -540,9 +543,7 @@ Job job(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& 
 cudaError_t make_pairs(const Jobs& jobs, int num_sms, cudaStream_t st) {
   const int64_t n = std::max(jobs.j[0].rows * jobs.j[0].ld, jobs.j[1].rows * jobs.j[1].ld) / 8;
   const int64_t blocks = std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 16);
-  pairs_kernel<<<(unsigned)blocks, 256, 0, st>>>(jobs);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError();
+  return launch_kernel(true, pairs_kernel, (unsigned)blocks, 256, 0, st, jobs);
 }
 
 // x and W as pairs; mx[0], mx[1] their largest magnitudes
@@ -553,9 +554,7 @@ cudaError_t operands(const GluArgs& a, unsigned* mx, const Pairs& x, const Pairs
   TRY(cudaMemsetAsync(mx, 0, 256, st));
   const int64_t n = std::max(a.M, 2 * a.F) * a.K;
   const int64_t blocks = std::min<int64_t>((n + 4095) / 4096, (int64_t)a.num_sms * 6);
-  largest_kernel<<<(unsigned)blocks, 256, 0, st>>>(jobs);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  TRY(cudaGetLastError());
+  TRY(launch_kernel(false, largest_kernel, (unsigned)blocks, 256, 0, st, jobs));
   return make_pairs(jobs, a.num_sms, st);
 }
 
@@ -596,7 +595,7 @@ cudaError_t glu_f32_forward(const GluArgs& a, cudaStream_t st) {
   P p = gated(a, mx);
   p.out = a.y; p.ld_out = a.F;
   p.tma_out = map_f32(&maps.out, a.y, a.F, a.M, 1, a.F);
-  return launch<kForward>(maps, p, a, st);
+  return launch<kForward>(maps, p, a, true, st);
 }
 
 cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
@@ -617,7 +616,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = dgu; p.ld_out = Fp;
     p.tma_out = map_f32(&maps.out, dgu, a.F, a.M, 2, Fp);
     p.omax = mx + 2;
-    TRY(launch<kDgu>(maps, p, a, st));
+    TRY(launch<kDgu>(maps, p, a, true, st));
   }
   Jobs jobs = {{job(dgu, 2 * a.M, a.F, Fp, d, mx + 2), job(nullptr, 0, 0, 0, d, mx + 3)}};
   TRY(make_pairs(jobs, a.num_sms, st));
@@ -642,7 +641,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = a.dx;
     p.tma_out = map_f32(&m.out, a.dx, a.K, a.M, 1, a.K);
     p.bmax = mx + 1;
-    TRY(launch<kDx>(m, p, a, st));
+    TRY(launch<kDx>(m, p, a, true, st));
   }
   if (a.dW) {
     Maps m = {};
@@ -659,7 +658,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = a.dW;
     p.tma_out = map_f32(&m.out, a.dW, a.K, a.F, 2, a.K);
     p.bmax = mx;
-    TRY(launch<kDw>(m, p, a, st));
+    TRY(launch<kDw>(m, p, a, true, st));
   }
   return cudaSuccess;
 }
