@@ -394,13 +394,14 @@ struct PadP {
 template <typename I>
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadP p) {
   next_may_start();
+  wait_for_last();
   const I per = (I)(p.ldd / 8), n0 = (I)p.rows[0] * per, total = n0 + (I)p.rows[1] * per;
   for (I i = (I)blockIdx.x * 256 + threadIdx.x; i < total; i += (I)gridDim.x * 256) {
     const int m = i >= n0;
     const I e = m ? i - n0 : i, r = e / per;
     const int c = (int)(e - r * per) * 8;
     const int64_t at = (int64_t)r * p.cols + c, last = (p.rows[m] * p.cols - 1) >> 3;
-    const uint4 q0 = __ldg(p.src[m] + (at >> 3)), q1 = __ldg(p.src[m] + min((at >> 3) + 1, last));
+    const uint4 q0 = __ldcs(p.src[m] + (at >> 3)), q1 = __ldcs(p.src[m] + min((at >> 3) + 1, last));
     const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
     const int skip = (int)(at & 7);  // values of the first piece before the row's
     uint32_t v[6], u[5], o[4];
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadP p) {
 }
 
 template <int PROD, int ACT>
-cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, bool after, cudaStream_t st) {
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
   auto kernel = glu_gemm_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
@@ -427,18 +428,18 @@ cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, bool after, cuda
   // few row tiles walked together keep their rows of A in L2 beside all of B
   p.group = std::min(p.m_tiles, 16);
   p.status = a.status;
-  e = launch_kernel(after, kernel, 2 * pairs, kThreads, kSmem, st, maps, p);
+  e = launch_kernel(kernel, 2 * pairs, kThreads, kSmem, 0, st, maps, p);
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
   return launch_join<bf16, kTile>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
-cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, bool after, cudaStream_t st) {
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
   if constexpr (PROD == kForward || PROD == kDgu) {
-    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, after, st);
-    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, after, st);
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
   }
-  return launch_act<PROD, 2>(maps, p, a, after, st);
+  return launch_act<PROD, 2>(maps, p, a, st);
 }
 
 // x and W with rows that TMA can read: as they are, or copied
@@ -466,8 +467,8 @@ cudaError_t operands(const GluArgs& a, char** ws, Operands* o, cudaStream_t st) 
   p.ldd = (int)o->ld;
   const int64_t work = (a.M + 2 * a.F) * (o->ld / 8);
   const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(work, 256), (int64_t)a.num_sms * 16);
-  return work < (int64_t(1) << 31) ? launch_kernel(false, pad_rows_kernel<uint32_t>, blocks, 256, 0, st, p)
-                                   : launch_kernel(false, pad_rows_kernel<int64_t>, blocks, 256, 0, st, p);
+  return work < (int64_t(1) << 31) ? launch_kernel(pad_rows_kernel<uint32_t>, blocks, 256, 0, 0, st, p)
+                                   : launch_kernel(pad_rows_kernel<int64_t>, blocks, 256, 0, 0, st, p);
 }
 
 }  // namespace
@@ -497,7 +498,7 @@ cudaError_t glu_tc_forward(const GluArgs& a, cudaStream_t st) {
   p.nkb = (int)ceil_div(a.K, 64);
   p.rows = (int)a.M; p.cols = (int)a.F;
   p.out = a.y; p.ld_out = a.F;
-  return launch<kForward>(maps, p, a, a.K % 8 != 0, st);
+  return launch<kForward>(maps, p, a, st);
 }
 
 cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
@@ -523,7 +524,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.nkb = (int)ceil_div(a.K, 64);
     p.rows = (int)a.M; p.cols = (int)a.F;
       p.dy = a.dy; p.ld_dy = a.F;
-    e = launch<kDgu>(maps, p, a, a.K % 8 != 0, st);
+    e = launch<kDgu>(maps, p, a, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dx) {
@@ -541,7 +542,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.rows = (int)a.M; p.cols = (int)a.K;
     p.out = a.dx; p.ld_out = a.K;
     p.part = part;
-    e = launch<kDx>(maps, p, a, true, st);
+    e = launch<kDx>(maps, p, a, st);
     if (e != cudaSuccess) return e;
   }
   if (a.dW) {
@@ -558,7 +559,7 @@ cudaError_t glu_tc_backward(const GluArgs& a, cudaStream_t st) {
     p.rows = (int)a.F; p.cols = (int)a.K;
     p.out = a.dW; p.ld_out = a.K;
     p.part = part;
-    e = launch<kDw>(maps, p, a, true, st);
+    e = launch<kDw>(maps, p, a, st);
   }
   return e;
 }

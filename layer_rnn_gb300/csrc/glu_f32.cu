@@ -347,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float* dy = static_cast<const float*>(p.dy) + (int64_t)(row0 + lane) * p.ld_dy + col + 4 * j;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                  if (col + 4 * j + u < p.cols) y[u] = __ldg(dy + u);
+                  if (col + 4 * j + u < p.cols) y[u] = __ldca(dy + u);
               }
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
@@ -390,25 +390,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int PROD, int ACT>
-cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, bool after, cudaStream_t st) {
+cudaError_t launch_act(const Maps& maps, P p, const GluArgs& a, cudaStream_t st) {
   auto kernel = glu_f32_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   const int pairs = plan_pairs(&p, a.num_sms, 8);  // 256 KB each way, three products a block
   p.group = std::min(p.m_tiles, 16);
   p.status = a.status;
-  e = launch_kernel(after, kernel, 2 * pairs, kThreads, kSmem, st, maps, p);
+  e = launch_kernel(kernel, 2 * pairs, kThreads, kSmem, 0, st, maps, p);
   const int64_t cut_tiles = (int64_t)p.m_tiles * p.n_tiles * p.planes - p.whole;
   if (e != cudaSuccess || cut_tiles == 0) return e;
   return launch_join<float, kCols>(p, cut_tiles, pairs, st);
 }
 template <int PROD>
-cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, bool after, cudaStream_t st) {
+cudaError_t launch(const Maps& maps, const P& p, const GluArgs& a, cudaStream_t st) {
   if constexpr (PROD == kForward || PROD == kDgu) {
-    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, after, st);
-    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, after, st);
+    if (a.act == 0) return launch_act<PROD, 0>(maps, p, a, st);
+    if (a.act == 1) return launch_act<PROD, 1>(maps, p, a, st);
   }
-  return launch_act<PROD, 2>(maps, p, a, after, st);
+  return launch_act<PROD, 2>(maps, p, a, st);
 }
 
 struct Pairs {
@@ -465,6 +465,7 @@ struct Jobs { Job j[2]; };
 // sources without gaps (lds = cols), on 16 bytes
 __global__ void __launch_bounds__(256) largest_kernel(const Jobs jobs) {
   next_may_start();
+  wait_for_last();
   __shared__ unsigned red[2][8];
   const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
 #pragma unroll
@@ -474,10 +475,10 @@ __global__ void __launch_bounds__(256) largest_kernel(const Jobs jobs) {
     unsigned m = 0;
 #pragma unroll 4
     for (int64_t i = first; i < n / 4; i += all) {
-      const float4 q = __ldg(v + i);
+      const float4 q = __ldca(v + i);
       m = max(max(m, max(magnitude(q.x), magnitude(q.y))), max(magnitude(q.z), magnitude(q.w)));
     }
-    if (first < n % 4) m = max(m, magnitude(__ldg(jobs.j[k].src + (n - n % 4) + first)));
+    if (first < n % 4) m = max(m, magnitude(__ldca(jobs.j[k].src + (n - n % 4) + first)));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = m;
   }
@@ -543,7 +544,7 @@ Job job(const float* src, int64_t rows, int64_t cols, int64_t lds, const Pairs& 
 cudaError_t make_pairs(const Jobs& jobs, int num_sms, cudaStream_t st) {
   const int64_t n = std::max(jobs.j[0].rows * jobs.j[0].ld, jobs.j[1].rows * jobs.j[1].ld) / 8;
   const int64_t blocks = std::min<int64_t>((n + 255) / 256, (int64_t)num_sms * 16);
-  return launch_kernel(true, pairs_kernel, (unsigned)blocks, 256, 0, st, jobs);
+  return launch_kernel(pairs_kernel, (unsigned)blocks, 256, 0, 0, st, jobs);
 }
 
 // x and W as pairs; mx[0], mx[1] their largest magnitudes
@@ -554,7 +555,7 @@ cudaError_t operands(const GluArgs& a, unsigned* mx, const Pairs& x, const Pairs
   TRY(cudaMemsetAsync(mx, 0, 256, st));
   const int64_t n = std::max(a.M, 2 * a.F) * a.K;
   const int64_t blocks = std::min<int64_t>((n + 4095) / 4096, (int64_t)a.num_sms * 6);
-  TRY(launch_kernel(false, largest_kernel, (unsigned)blocks, 256, 0, st, jobs));
+  TRY(launch_kernel(largest_kernel, (unsigned)blocks, 256, 0, 0, st, jobs));
   return make_pairs(jobs, a.num_sms, st);
 }
 
@@ -595,7 +596,7 @@ cudaError_t glu_f32_forward(const GluArgs& a, cudaStream_t st) {
   P p = gated(a, mx);
   p.out = a.y; p.ld_out = a.F;
   p.tma_out = map_f32(&maps.out, a.y, a.F, a.M, 1, a.F);
-  return launch<kForward>(maps, p, a, true, st);
+  return launch<kForward>(maps, p, a, st);
 }
 
 cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
@@ -616,7 +617,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = dgu; p.ld_out = Fp;
     p.tma_out = map_f32(&maps.out, dgu, a.F, a.M, 2, Fp);
     p.omax = mx + 2;
-    TRY(launch<kDgu>(maps, p, a, true, st));
+    TRY(launch<kDgu>(maps, p, a, st));
   }
   Jobs jobs = {{job(dgu, 2 * a.M, a.F, Fp, d, mx + 2), job(nullptr, 0, 0, 0, d, mx + 3)}};
   TRY(make_pairs(jobs, a.num_sms, st));
@@ -641,7 +642,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = a.dx;
     p.tma_out = map_f32(&m.out, a.dx, a.K, a.M, 1, a.K);
     p.bmax = mx + 1;
-    TRY(launch<kDx>(m, p, a, true, st));
+    TRY(launch<kDx>(m, p, a, st));
   }
   if (a.dW) {
     Maps m = {};
@@ -658,7 +659,7 @@ cudaError_t glu_f32_backward(const GluArgs& a, cudaStream_t st) {
     p.out = a.dW;
     p.tma_out = map_f32(&m.out, a.dW, a.K, a.F, 2, a.K);
     p.bmax = mx;
-    TRY(launch<kDw>(m, p, a, true, st));
+    TRY(launch<kDw>(m, p, a, st));
   }
   return cudaSuccess;
 }

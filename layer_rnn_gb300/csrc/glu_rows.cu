@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "glu.cuh"
+#include "launch.cuh"
 #include "ops.h"
 
 namespace lr {
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(kThreads) glu_rows_kernel(const RowsP p) {
       w[slot][u][1] = __ldcs(up + at);
     }
   };
+  next_may_start();
+  wait_for_last();
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(i, i);
 
@@ -249,20 +252,7 @@ cudaError_t launch_rows(RowsP p, int csize, cudaStream_t st) {
   if (smem > 48 * 1024)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.F + kFeatures - 1) / kFeatures * csize));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)csize;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 1 : 0;  // a launch with the attribute takes 2 us longer
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
+  return launch_kernel(kernel, (unsigned)((p.F + kFeatures - 1) / kFeatures * csize), kThreads, smem, csize, st, p);
 }
 
 // tokens in passes of 32 at most, fewer where x would not fit eight blocks

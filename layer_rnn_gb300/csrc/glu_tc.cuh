@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "glu.cuh"
+#include "launch.cuh"
 #include "ops.h"
 #include "wait.cuh"
 
@@ -188,32 +189,6 @@ __device__ __forceinline__ float4* part_at(const P& p, int64_t slot, int part) {
   return reinterpret_cast<float4*>(p.part) + (slot * 8 + part) * (TN / 4 * 32);
 }
 
-// Kernels of one call follow each other without a gap: each is launched while the
-// one before it still runs, sets itself up, and waits for its end, and so for all
-// before it, where it first touches memory.  The first of a call is launched as
-// usual.
-__device__ __forceinline__ void next_may_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <typename... P, typename... A>
-cudaError_t launch_kernel(bool after, void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
-                          cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
-}
-
 // Joins the partial tiles: block x handles four columns of 32 rows for each of its
 // warps, in one cut tile's eighth (block of the pair * 4 + row quarter).  Pairs in
 // rising order.
@@ -254,7 +229,7 @@ __global__ void __launch_bounds__(256) glu_join_kernel(const P p, int pairs) {
 }
 template <typename E, int TN>
 cudaError_t launch_join(const P& p, int64_t cut_tiles, int pairs, cudaStream_t st) {
-  return launch_kernel(true, glu_join_kernel<E, TN>, (unsigned)(cut_tiles * 8 * (TN / 4 * 32 / 256)), 256, 0,
+  return launch_kernel(glu_join_kernel<E, TN>, (unsigned)(cut_tiles * 8 * (TN / 4 * 32 / 256)), 256, 0, 0,
                        st, p, pairs);
 }
 

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "ops.h"
 #include "wait.cuh"
 
@@ -217,14 +218,14 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 
 // a lane's word from memory and to it; n: how many of its channels exist
 __device__ __forceinline__ uint32_t get_word(const float* p, int n) {
-  return n > 0 ? __float_as_uint(__ldg(p)) : 0u;
+  return n > 0 ? __float_as_uint(__ldca(p)) : 0u;
 }
 __device__ __forceinline__ uint32_t get_word(const bf16* p, int n) {
   const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
-  if (n == 2 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) return __ldg(reinterpret_cast<const unsigned*>(p));
+  if (n == 2 && (reinterpret_cast<uintptr_t>(p) & 3) == 0) return __ldca(reinterpret_cast<const unsigned*>(p));
   uint32_t w = 0;
-  if (n > 0) w = __ldg(h);
-  if (n > 1) w |= (uint32_t)__ldg(h + 1) << 16;
+  if (n > 0) w = __ldca(h);
+  if (n > 1) w |= (uint32_t)__ldca(h + 1) << 16;
   return w;
 }
 __device__ __forceinline__ void put_word(float* p, uint32_t w, int n) {
@@ -394,8 +395,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
   __shared__ __align__(16) MapV<V> map[2][kWarps][32];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const unsigned csize = cluster_size(), rank = cluster_rank();
-  const Place<E> at(p, (int)(blockIdx.x / csize));
   Ring ring(smem_raw, bars, ST + 2);
+  next_may_start();
+  wait_for_last();
+  const Place<E> at(p, (int)(blockIdx.x / csize));
   // the cluster's tiles: [parity of the round][block][lane]
   MapV<V>* tile_map = reinterpret_cast<MapV<V>*>(smem_raw + (ring.base - tc::smem_addr(smem_raw)) + ST * kStage);
   const int rounds = (int)((p.T + (int64_t)kTileSteps * csize - 1) / ((int64_t)kTileSteps * csize));
@@ -565,8 +568,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
   __shared__ float forth[2][kWarps][V][32];             // B of the walk's maps
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const unsigned csize = cluster_size(), rank = cluster_rank();
-  const Place<E> at(p, (int)(blockIdx.x / csize));
   Ring ring(smem_raw, bars, ST + 2);
+  next_may_start();
+  wait_for_last();
+  const Place<E> at(p, (int)(blockIdx.x / csize));
   MapV<V>* tile_map = reinterpret_cast<MapV<V>*>(smem_raw + (ring.base - tc::smem_addr(smem_raw)) + ST * kStage);
   const int tiles = (p.T + kTileSteps - 1) / kTileSteps;
   const int rounds = (int)((tiles + (int64_t)csize - 1) / csize);
@@ -594,7 +599,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
     const int64_t tile = tile_of(r);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      h[v] = r < rounds && active(tile) && v < at.live ? __ldg(p.states + tile * states_row + at.gh + v) : 0.f;
+      h[v] = r < rounds && active(tile) && v < at.live ? __ldca(p.states + tile * states_row + at.gh + v) : 0.f;
   };
   float carry[V], next[V];
 #pragma unroll
@@ -767,6 +772,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
 template <typename E, int V, bool GATE>
 __global__ void __launch_bounds__(kThreads) scan_steps_kernel(const ScanP p) {
   constexpr int G = GATE ? 3 : 2;
+  next_may_start();
+  wait_for_last();
   const Lane l = lane_of(p, (int64_t)blockIdx.x * kThreads + threadIdx.x, V, G);
   if (!l.live) return;
   const E* gx = static_cast<const E*>(p.gx) + l.g0;
@@ -873,20 +880,7 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
   if (e == cudaSuccess && csize > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(groups * csize));
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)csize;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = csize > 1 ? 1 : 0;  // a launch with the attribute takes 2 us longer
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
+  return launch_kernel(kernel, (unsigned)(groups * csize), 32 * kWarps, smem, (unsigned)csize, st, p);
 }
 
 // Stages of the ring: two tiles in flight a block.  A third leaves room for
@@ -909,10 +903,8 @@ template <typename E, int V>
 cudaError_t forward_steps(const ScanArgs& a, cudaStream_t st) {
   const ScanP p = params(a, V);
   const unsigned blocks = (unsigned)((p.vecs + kThreads - 1) / kThreads);
-  if (a.gate) scan_steps_kernel<E, V, true><<<blocks, kThreads, 0, st>>>(p);
-  else scan_steps_kernel<E, V, false><<<blocks, kThreads, 0, st>>>(p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return cudaGetLastError();
+  return a.gate ? launch_kernel(scan_steps_kernel<E, V, true>, blocks, kThreads, 0, 0, st, p)
+                : launch_kernel(scan_steps_kernel<E, V, false>, blocks, kThreads, 0, 0, st, p);
 }
 
 }  // namespace

@@ -38,6 +38,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "ops.h"
 
 namespace lr {
@@ -148,10 +149,10 @@ __device__ __forceinline__ Four get_four(const W4P& p, int kb, int m) {
   if (p.K % 4 == 0) {
     if (k < p.K) {
       if (F32) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + x0));
+        const float4 q = __ldca(reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + x0));
         r.v[0] = q.x; r.v[1] = q.y; r.v[2] = q.z; r.v[3] = q.w;
       } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(p.x) + x0));
+        const uint2 q = __ldca(reinterpret_cast<const uint2*>(static_cast<const bf16*>(p.x) + x0));
         r.v[0] = __uint_as_float(q.x << 16); r.v[1] = __uint_as_float(q.x & 0xffff0000u);
         r.v[2] = __uint_as_float(q.y << 16); r.v[3] = __uint_as_float(q.y & 0xffff0000u);
       }
@@ -160,8 +161,8 @@ __device__ __forceinline__ Four get_four(const W4P& p, int kb, int m) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (k + u < p.K)
-        r.v[u] = F32 ? __ldg(static_cast<const float*>(p.x) + x0 + u)
-                     : __uint_as_float((uint32_t)__ldg(static_cast<const unsigned short*>(p.x) + x0 + u) << 16);
+        r.v[u] = F32 ? __ldca(static_cast<const float*>(p.x) + x0 + u)
+                     : __uint_as_float((uint32_t)__ldca(static_cast<const unsigned short*>(p.x) + x0 + u) << 16);
   }
   return r;
 }
@@ -255,11 +256,13 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
       for (int h = 0; h < 2; ++h) {
         w[slot][mt][h] = __ldcs(reinterpret_cast<const uint4*>(wbase + (wo[mt][h] + piece)));
         const uint32_t at = so[mt][h] + gi;
-        sc[slot][mt][h] = F32 ? __ldg(reinterpret_cast<const unsigned*>(sbase + (size_t)(at * 4u)))
-                              : (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(sbase + (size_t)(at * 2u)));
-        if (ZERO) zp[ZERO ? slot : 0][mt][h] = __ldg(zbase + at);
+        sc[slot][mt][h] = F32 ? __ldca(reinterpret_cast<const unsigned*>(sbase + (size_t)(at * 4u)))
+                              : (uint32_t)__ldca(reinterpret_cast<const unsigned short*>(sbase + (size_t)(at * 2u)));
+        if (ZERO) zp[ZERO ? slot : 0][mt][h] = __ldca(zbase + at);
       }
   };
+  next_may_start();
+  wait_for_last();
 #pragma unroll
   for (int i = 0; i < D; ++i) fetch(i, i);
 
@@ -476,20 +479,7 @@ cudaError_t launch(W4P p, const W4Args& a, cudaStream_t st) {
   if (smem > 48 * 1024)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(blocks * c));
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)c;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = c > 1 ? 1 : 0;  // a launch with the attribute takes 2 us longer
-  e = cudaLaunchKernelEx(&cfg, kernel, p);
-  g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
+  return launch_kernel(kernel, (unsigned)(blocks * c), 32 * kWarps, smem, (unsigned)c, st, p);
 }
 
 template <bool F32, int NT, int MT, int NW, int WK>
