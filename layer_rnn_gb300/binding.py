@@ -392,9 +392,13 @@ class Ops:
         self.torch = torch
         self.dtype = dtype
         self.tdtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self._u8, self._f32 = torch.uint8, torch.float32
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._device = torch._C._cuda_getDevice if self._raw_stream is not None else None
-        self._lib = lib()
+        # the entry points of a step's calls: looking them up by name is 0.2 us of six
+        L = lib()
+        self._scan_step, self._w4_matvec = L.rnn_scan_step, L.rnn_w4_matvec
+        self._glu_forward = L.rnn_glu_forward
         self.h = None
         h = _vp()
         _call("rnn_ops_create", ctypes.byref(h), DTYPES[dtype], flags)
@@ -430,6 +434,14 @@ class Ops:
         if not t.is_cuda or not t.is_contiguous():
             raise ValueError("%s: expected a contiguous CUDA tensor" % name)
         return t.data_ptr()
+
+    def _on(self, stream, t):
+        """The stream's address: the given one, or the current one of t's device."""
+        if stream is None and self._raw_stream is not None:
+            d = t.get_device()
+            if d >= 0:
+                return self._raw_stream(d)
+        return self._stream(stream)
 
     def _rows(self, name, t, shape, pitch=None):
         """A tensor [..., width] whose rows are evenly spaced: address, pitch."""
@@ -492,12 +504,14 @@ class Ops:
         """One token: gx [N, G*H], state and state_out [N, H] (may be the same
         tensor), y [N, H]."""
         N, H = state.shape
-        f32 = self.torch.float32
+        f32 = self._f32
         pg, ldg = self._rows("gx", gx, (N, (3 if out_gate else 2) * H))
         py, ldy = self._rows("y", y, (N, H))
-        _call("rnn_scan_step", self.h, self._stream(stream), N, H, int(out_gate), pg, ldg,
-              self._check("state", state, (N, H), f32),
-              self._check("state_out", state_out, (N, H), f32), py, ldy)
+        code = self._scan_step(self.h, self._on(stream, gx), N, H, int(out_gate), pg, ldg,
+                               self._check("state", state, (N, H), f32),
+                               self._check("state_out", state_out, (N, H), f32), py, ldy)
+        if code:
+            raise RnnError("rnn_scan_step", code)
 
     # -- gated feed-forward -------------------------------------------------------
     def glu_workspace_bytes(self, M, K, F, backward=False):
@@ -508,9 +522,11 @@ class Ops:
     def glu_forward(self, x, W, y, ws, act="silu", stream=None):
         """y [M, F] = act(x Wg^T) * (x Wu^T), x [M, K], W = [Wg; Wu] [2F, K]."""
         (M, K), F = x.shape, W.shape[0] // 2
-        _call("rnn_glu_forward", self.h, self._stream(stream), M, K, F, ACTS[act],
-              self._check("x", x, (M, K)), self._check("W", W, (2 * F, K)),
-              self._check("y", y, (M, F)), _p(ws), ws.numel() * ws.element_size())
+        code = self._glu_forward(self.h, self._on(stream, x), M, K, F, ACTS[act],
+                                 self._check("x", x, (M, K)), self._check("W", W, (2 * F, K)),
+                                 self._check("y", y, (M, F)), ws.data_ptr(), ws.nbytes)
+        if code:
+            raise RnnError("rnn_glu_forward", code)
 
     def glu_backward(self, x, W, dy, dx, dW, ws, act="silu", stream=None):
         """dx [M, K] and dW [2F, K] (either may be None)."""
@@ -539,9 +555,12 @@ class Ops:
 
     def w4_matvec(self, x, q, scales, y, group=128, zeros=None, stream=None):
         """y [M, R] = x [M, K] times the 4-bit weights [R, K] transposed."""
-        (M, K), R = x.shape, q.shape[0]
-        groups, u8 = (K + group - 1) // group, self.torch.uint8
-        _call("rnn_w4_matvec", self.h, self._stream(stream), M, R, K, group,
-              self._check("x", x, (M, K)), self._check("q", q, (R, q.shape[1]), u8), q.shape[1],
-              self._check("scales", scales, (R, groups)), self._check("zeros", zeros, (R, groups), u8),
-              self._check("y", y, (M, R)))
+        (M, K), (R, ldq) = x.shape, q.shape
+        groups, u8 = (K + group - 1) // group, self._u8
+        code = self._w4_matvec(self.h, self._on(stream, x), M, R, K, group, self._check("x", x, (M, K)),
+                               self._check("q", q, (R, ldq), u8), ldq,
+                               self._check("scales", scales, (R, groups)),
+                               self._check("zeros", zeros, (R, groups), u8),
+                               self._check("y", y, (M, R)))
+        if code:
+            raise RnnError("rnn_w4_matvec", code)
