@@ -14,7 +14,7 @@
 //   exactly;
 // - no shared memory, barrier or address arithmetic for the weights: a ring
 //   of them (by TMA) took 24 more instructions for 16 x 32 weights, and the
-//   kernel 31 us where this one takes 21 (32768 x 4096, one token: 70 MB, 3.3 TB/s).  e4m3
+//   kernel 31 us where loads to registers took 21 (32768 x 4096, one token).  e4m3
 //   operands, into which nibbles turn with a mask, are converted to fp16 by the
 //   product itself here and saved nothing.
 // Where a group is 128 weights, the four lanes of a row take 32 of them each;
@@ -27,12 +27,14 @@
 // x s = hi + lo 2^-11, 22 bits of every value near the largest.  Products are
 // exact; each group is summed in float32 and only then multiplied by its scale.
 //
-// The four warps of a block take different rows, or, where the rows alone do not
-// fill the card, the same rows and different parts of K; blocks of a cluster
-// split K where it would not, or where x would not fit.  Partial sums are
-// joined in a fixed order.  For 5 to 16 tokens making the columns takes as long as
-// two row tiles of the product, so eight warps share them and take several row
-// tiles each (16384 x 6007, 8 float32 tokens: 40.0 us with one tile, 35.6 with two).
+// The warps of a block take different rows and, where rows alone do not fill the
+// card, different parts of K; blocks of a cluster split K where x would not fit, or
+// where there are too few rows (make_plan).  Partial sums are joined in a fixed
+// order.
+//
+// Bound by the instructions that unpack, with latency on top: 32768 x 4096, one
+// token, group 128: 18.9 us (10.5 at the copy rate); 16384 x 6007, eight float32
+// tokens, group 32, zero points: 32.2 us (9.5).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -46,7 +48,9 @@ namespace {
 
 constexpr int kBlockK = 128;        // weights of a row in one step
 constexpr int kTokens = 16;         // of a pass at most
-constexpr int kXBytes = 64 * 1024;  // x of one block at most; beyond half of it K is split sooner
+constexpr int kXBytes = 160 * 1024;  // x of a block, where K is split over eight
+constexpr int kMostWarps = 16;      // of a block: 128 registers a thread
+constexpr int kMostRows = 1024;     // of a block: times 2^22 bytes, offsets fit 32 bits
 
 struct W4P {
   int M, R, K, nkb, groups, m0, toks;  // tokens m0 .. m0 + toks
@@ -57,6 +61,7 @@ struct W4P {
   const uint8_t* zeros;
   void* y;
   int x_bytes;                         // shared memory of the columns
+  int rw, wk;                          // warps of a block: along rows, along K
   int turns;                           // row tiles that each warp takes in turn
 };
 
@@ -201,25 +206,24 @@ __device__ __forceinline__ void make_columns(const Four& x, int m, unsigned char
 }
 
 // F32: element type float32 (two columns a token), else bf16.  NT: column
-// tiles of 8; MT: row tiles of 16 a warp; kWarps of a block; WK: of them, those
-// that split K (1 or all); GS: 32-weight chunks a group.
-template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
-__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P p) {
+// tiles of 8; MT: row tiles of 16 a warp; GS: 32-weight chunks a group.
+template <bool F32, int NT, int MT, int GS, bool ZERO>
+__global__ void __launch_bounds__(32 * kMostWarps, 1) w4_kernel(const W4P p) {
   extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kThreads = 32 * kWarps;
-  constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
-  constexpr int D = MT == 1 ? 4 : 3;         // steps whose loads are under way
-  constexpr bool kDirect = GS == 4, kTurns = kWarps == 8;
+  constexpr int kRows = 16 * MT;
+  constexpr int D = MT == 2 ? 2 : NT == 4 ? 3 : 4;  // steps whose loads are under way (registers)
+  constexpr bool kDirect = GS == 4;
   constexpr int kTok = F32 ? 1 : 2;          // tokens of a lane and column tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const unsigned csize = cl_size(), rank = cl_rank();
   if (csize > 1) cl_arrive();  // every block runs before the first is written to
   const int cols = F32 ? 2 * p.toks : p.toks;
-  const int turns = kTurns ? p.turns : 1, rows_all = kBlockRows * turns;  // of the block
+  const int warps = p.rw * p.wk, along = warp % p.wk, beside = warp / p.wk;
+  const int turns = p.turns, rows_turn = p.rw * kRows, rows_all = rows_turn * turns;  // of the block
   const int block0 = (int)(blockIdx.x / csize) * rows_all;
   const int kb0 = (int)((int64_t)rank * p.nkb / csize), kb1 = (int)((int64_t)(rank + 1) * p.nkb / csize);
-  const int first = kb0 + (WK == 1 ? 0 : warp);
-  const int steps = first < kb1 ? (kb1 - first + WK - 1) / WK : 0;
+  const int first = kb0 + along * (kb1 - kb0) / p.wk;
+  const int steps = kb0 + (along + 1) * (kb1 - kb0) / p.wk - first;
   float* muls = reinterpret_cast<float*>(smem + p.x_bytes);  // [block of 128][kTokens]
 
   // Nothing in the loop asks whether a row, a piece or a column exists: rows past
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
   const uint8_t* zbase = p.zeros + (int64_t)block0 * p.groups;
   uint32_t wo[MT][2], so[MT][2];
   auto set_rows = [&](int turn) {
-    const int row0 = block0 + turn * kBlockRows + (WK == 1 ? warp * kRows : 0);
+    const int row0 = block0 + turn * rows_turn + beside * kRows;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
   uint32_t sc[D][MT][2], zp[ZERO ? D : 1][MT][2];
   auto fetch = [&](int slot, int i) {
     if (i >= steps) return;
-    const int kb = first + i * WK;
+    const int kb = first + i;
     const uint32_t piece = min((uint32_t)(kb * 64 + t * 16), (uint32_t)p.ldq - 16u);
     // a block's 4 / GS groups: lane t has group t of them
     const uint32_t gi = (uint32_t)min(kb * (4 / GS) + (GS == 4 ? 0 : GS == 2 ? (t & 1) : t), p.groups - 1);
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
 
   // x: eight loads of a warp under way at a time, pair e of (block, token)
   constexpr int kBatch = 8;
-  const int nb = kb1 - kb0, db = kWarps / p.toks, dm = kWarps - db * p.toks;
+  const int nb = kb1 - kb0, db = warps / p.toks, dm = warps - db * p.toks;
   int b = warp / p.toks, m = warp - b * p.toks;
   while (b < nb) {
     Four x[kBatch];
@@ -401,8 +405,8 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
               fin[mt][nt][i] = fmaf(mul[nt][i % kTok], part[mt][nt][i], fin[mt][nt][i]);
         fetch(slot, i0 + slot + D);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xa[nt] += WK * 4 * x_chunk;
-        ma += WK * kTokens;
+        for (int nt = 0; nt < NT; ++nt) xa[nt] += 4 * x_chunk;
+        ma += kTokens;
       }
     }
 
@@ -422,20 +426,19 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
 #pragma unroll
           for (int k = 0; k < kTok; ++k) {
             const int m = (nt * 4 + t) * kTok + k;
-            const int r = turn * kBlockRows + (WK == 1 ? warp * kRows : 0) + mt * 16 + h * 8 + g;
+            const int r = turn * rows_turn + beside * kRows + mt * 16 + h * 8 + g;
             const float v = fin[mt][nt][h * kTok + k];
             if (m >= p.toks) continue;
-            if (WK > 1) within[warp * share + m * rows_all + r] = v;
+            if (p.wk > 1) within[along * share + m * rows_all + r] = v;
             else if (csize > 1) st_rank0(across + (int)rank * share + m * rows_all + r, v);
             else put(block0 + r, m, v);
           }
   }
-  if (WK > 1) {
+  if (p.wk > 1) {
     __syncthreads();
-    for (int i = threadIdx.x; i < share; i += kThreads) {
+    for (int i = threadIdx.x; i < share; i += 32 * warps) {
       float v = 0.f;
-#pragma unroll
-      for (int u = 0; u < kWarps; ++u) v += within[u * share + i];
+      for (int u = 0; u < p.wk; ++u) v += within[u * share + i];
       if (csize > 1) st_rank0(across + (int)rank * share + i, v);
       else put(block0 + i % rows_all, i / rows_all, v);
     }
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
     cl_arrive();
     cl_wait();
     if (rank == 0)
-      for (int i = threadIdx.x; i < share; i += kThreads) {
+      for (int i = threadIdx.x; i < share; i += 32 * warps) {
         float v = 0.f;
         for (unsigned c = 0; c < csize; ++c) v += across[c * share + i];
         put(block0 + i % rows_all, i / rows_all, v);
@@ -453,56 +456,77 @@ __global__ void __launch_bounds__(32 * kWarps, 16 / kWarps) w4_kernel(const W4P 
   }
 }
 
-template <bool F32, int NT, int MT, int kWarps, int WK, int GS, bool ZERO>
-cudaError_t launch(W4P p, const W4Args& a, cudaStream_t st) {
-  auto kernel = w4_kernel<F32, NT, MT, kWarps, WK, GS, ZERO>;
-  constexpr int kRows = 16 * MT, kBlockRows = WK == 1 ? kWarps * kRows : kRows;
-  int blocks = (p.R + kBlockRows - 1) / kBlockRows;
-  // K over the blocks of a cluster: until x fits, and until the card has two
-  // blocks an SM as long as each warp keeps four steps
-  const int cols = p.toks * (F32 ? 2 : 1);
-  auto x_of = [&](int c) { return (p.nkb + c - 1) / c * cols * 256; };
-  int c = 1;
-  while (c < 8 && x_of(c) > (kWarps == 8 ? kXBytes : kXBytes / 2)) c *= 2;
-  while (c < 8 && blocks * c < 2 * a.num_sms && p.nkb >= 8 * c * WK) c *= 2;
-  // eight warps a block are two blocks an SM: more than they hold at once take up to
-  // four row tiles a warp, for columns that are made once
-  p.turns = 1;
-  if (kWarps == 8) {
-    p.turns = std::max(1, std::min(4, (blocks * c + 2 * a.num_sms - 1) / (2 * a.num_sms)));
-    blocks = (blocks + p.turns - 1) / p.turns;
+// How the warps of a block, the blocks and the blocks of a cluster share the work.
+// Time is counted in a warp's steps (16 MT rows, 128 k): the warps of an SM take turns
+// at issuing, and with fewer than kHide of them a step takes its latency.  A column's
+// making is a third of a step, a cluster's exchange about 1 us.  Blocks are as high as
+// fills the SMs evenly, one, two or four on each.  32768 x 4096, one token: 19.2 us with
+// seven warps along rows and two along K, one block an SM; 20.3 with four along rows in
+// clusters of two, of which some SMs had four and some three; 24 with four along K.
+// 16384 x 6007, eight float32 tokens: 32.4 us with 14 along rows in clusters of two, 36
+// with eight in clusters of four, each taking two row tiles, 41 with seven and two along K.
+struct Plan { int rw = 0, wk = 1, c = 1, turns = 1, slots = 1; };
+constexpr int kHide = 12, kRoom = 216 * 1024;
+int64_t smem_of(const W4P& p, const Plan& q, int rows_warp, int cols) {
+  const int nb = (p.nkb + q.c - 1) / q.c;
+  return (int64_t)nb * (cols * 256 + kTokens * 4) +
+         (int64_t)((q.c > 1 ? q.c : 0) + (q.wk > 1 ? q.wk : 0)) * p.toks * q.rw * rows_warp * q.turns * 4;
+}
+Plan make_plan(const W4P& p, int rows_warp, int cols, int num_sms) {
+  const int tiles = (p.R - 1) / rows_warp + 1;
+  int c0 = 1;  // the fewest blocks of a cluster in which x fits
+  while (c0 < 8 && (int64_t)((p.nkb + c0 - 1) / c0) * (cols * 256 + kTokens * 4) > kRoom - 32 * 1024) c0 *= 2;
+  Plan best, q;
+  float least = 0.f;
+  for (q.c = c0; q.c <= 8 && (q.c == c0 || (q.c <= p.nkb && (q.c == 2 * c0 || tiles * q.c <= num_sms))); q.c *= 2) {
+    const int nb = (p.nkb + q.c - 1) / q.c;
+    for (q.wk = 1; q.wk <= 4 && (q.wk == 1 || 2 * q.wk <= nb); q.wk *= 2) {
+      for (q.slots = 1; q.slots * q.wk <= kMostWarps && q.slots <= 4; q.slots *= 2) {
+        const int fit = std::max(1, num_sms * q.slots / q.c);  // blocks, or clusters, at once
+        q.rw = std::min(kMostWarps / (q.slots * q.wk), (tiles - 1) / fit + 1);
+        if ((smem_of(p, q, rows_warp, cols) + 1024) * q.slots > kRoom) continue;
+        const int blocks = (tiles - 1) / q.rw + 1, rounds = (blocks - 1) / fit + 1, warps = q.rw * q.wk;
+        const int busy = std::min(q.slots, (blocks * q.c - 1) / num_sms + 1) * warps;
+        const float steps = (float)((nb - 1) / q.wk + 1) + (float)(p.toks * nb) / (3.f * (float)warps) + 2.f;
+        const float t = (float)rounds * steps * (float)std::max(kHide, busy) + (q.c > 1 ? 24.f : 0.f);
+        if (best.rw == 0 || t < least) {
+          best = q;
+          least = t;
+        }
+      }
+    }
   }
-  p.x_bytes = x_of(c);
-  const size_t smem = (size_t)p.x_bytes + (p.nkb + c - 1) / c * kTokens * 4 +
-                      (size_t)((c > 1 ? c : 0) + (WK > 1 ? kWarps : 0)) * p.toks * kBlockRows * p.turns * 4;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kernel, (unsigned)(blocks * c), 32 * kWarps, smem, (unsigned)c, st, p);
+  if (best.rw == 0) return best;
+  // more blocks than fit at once: fewer that take several row tiles a warp
+  const int fit = std::max(1, num_sms * best.slots / best.c), blocks = (tiles - 1) / best.rw + 1;
+  q = best;
+  q.turns = std::min((blocks - 1) / fit + 1, std::max(1, kMostRows / (best.rw * rows_warp)));
+  return (smem_of(p, q, rows_warp, cols) + 1024) * q.slots <= kRoom ? q : best;
 }
 
-template <bool F32, int NT, int MT, int NW, int WK>
+template <bool F32, int NT, int MT, int GS, bool ZERO>
+cudaError_t launch(W4P p, const Plan& q, cudaStream_t st) {
+  auto kernel = w4_kernel<F32, NT, MT, GS, ZERO>;
+  const int cols = p.toks * (F32 ? 2 : 1), rows = q.rw * 16 * MT * q.turns;
+  p.x_bytes = (p.nkb + q.c - 1) / q.c * cols * 256;
+  p.rw = q.rw; p.wk = q.wk; p.turns = q.turns;
+  const size_t smem = (size_t)smem_of(p, q, 16 * MT, cols);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernel(kernel, (unsigned)(((int64_t)p.R + rows - 1) / rows * q.c), 32 * q.rw * q.wk, smem,
+                       (unsigned)q.c, st, p);
+}
+
+template <bool F32, int NT, int MT>
 cudaError_t by_group(const W4P& p, const W4Args& a, cudaStream_t st) {
+  const Plan q = make_plan(p, 16 * MT, p.toks * (F32 ? 2 : 1), a.num_sms);
+  if (q.rw == 0) return cudaErrorInvalidValue;
   const bool z = a.zeros != nullptr;
-  if (a.group == 32)
-    return z ? launch<F32, NT, MT, NW, WK, 1, true>(p, a, st)
-             : launch<F32, NT, MT, NW, WK, 1, false>(p, a, st);
-  if (a.group == 64)
-    return z ? launch<F32, NT, MT, NW, WK, 2, true>(p, a, st)
-             : launch<F32, NT, MT, NW, WK, 2, false>(p, a, st);
-  return z ? launch<F32, NT, MT, NW, WK, 4, true>(p, a, st)
-           : launch<F32, NT, MT, NW, WK, 4, false>(p, a, st);
-}
-
-// NW warps take different rows; four split K where rows in blocks of 16 MT NW, and
-// K split over clusters, would give the card less than two blocks an SM.
-template <bool F32, int NT, int MT, int NW>
-cudaError_t by_rows(const W4P& p, const W4Args& a, cudaStream_t st) {
-  const int64_t blocks =
-      (a.R + 16 * MT * NW - 1) / (16 * MT * NW) * std::max(1, std::min(8, p.nkb / 4));
-  return blocks >= 2 * a.num_sms ? by_group<F32, NT, MT, NW, 1>(p, a, st)
-                                 : by_group<F32, NT, 1, 4, 4>(p, a, st);
+  if (a.group == 32) return z ? launch<F32, NT, MT, 1, true>(p, q, st) : launch<F32, NT, MT, 1, false>(p, q, st);
+  if (a.group == 64) return z ? launch<F32, NT, MT, 2, true>(p, q, st) : launch<F32, NT, MT, 2, false>(p, q, st);
+  return z ? launch<F32, NT, MT, 4, true>(p, q, st) : launch<F32, NT, MT, 4, false>(p, q, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -566,14 +590,13 @@ cudaError_t w4_matvec(const W4Args& a, cudaStream_t st) {
     p.m0 = (int)m0;
     p.toks = (int)std::min<int64_t>(tok, a.M - m0);
     cudaError_t e;
-    // two row tiles a warp where registers allow four blocks an SM with them; eight
-    // warps to a block's x where making its columns is a good part of the work
+    // two row tiles a warp where 128 registers hold them
     if (a.bf16)
-      e = p.toks <= 8 ? by_rows<false, 1, 2, 4>(p, a, st) : by_rows<false, 2, 1, 8>(p, a, st);
+      e = p.toks <= 8 ? by_group<false, 1, 2>(p, a, st) : by_group<false, 2, 1>(p, a, st);
     else
-      e = p.toks <= 4   ? by_rows<true, 1, 1, 4>(p, a, st)
-          : p.toks <= 8 ? by_rows<true, 2, 1, 8>(p, a, st)
-                        : by_rows<true, 4, 1, 8>(p, a, st);
+      e = p.toks <= 4   ? by_group<true, 1, 1>(p, a, st)
+          : p.toks <= 8 ? by_group<true, 2, 1>(p, a, st)
+                        : by_group<true, 4, 1>(p, a, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
