@@ -557,8 +557,10 @@ __global__ void __launch_bounds__(32 * kWarps, 3)
   if (csize > 1) cluster_sync();  // no block leaves before the others' stores to it
 }
 
+// Blocks an SM: three, or four where registers and the ring (48 KB) allow them: both
+// directions of 300 x 20 x 800 in float32, 52.1 -> 50.0 us with the forward.
 template <typename E, bool GATE, bool TMA, int ST>
-__global__ void __launch_bounds__(32 * kWarps, 3)
+__global__ void __launch_bounds__(32 * kWarps, TMA && !GATE && sizeof(E) == 4 ? 4 : 3)
     scan_backward_tiles(const __grid_constant__ TileP p) {
   constexpr int G = GATE ? 3 : 2, V = Word<E>::V, L = kSteps;
   constexpr int kStage = TMA ? (G + 1) * kPlane : 0;
