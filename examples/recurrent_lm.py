@@ -92,7 +92,7 @@ class Model:
         self.layers = [dict(gates=weight(3 * H, width), out=weight(width, H), up=weight(2 * F, width),
                             down=weight(width, F)) for _ in range(layers)]
         with torch.no_grad():
-            for k, layer in enumerate(self.layers):  # rows scaled apart: some gates remember long
+            for layer in self.layers:  # wider forget gates: some channels remember long
                 layer["gates"][:H] *= 2.0
 
     def parameters(self):

@@ -9,7 +9,7 @@
 // product is free: a lane's 16-byte piece of a row goes from memory into the
 // registers that are the operand, four steps ahead of its use, with no shared
 // memory or barrier between.  (A ring of asynchronous copies took 7.3 us where
-// this takes 6.5: one token, 1024 x 4096, weights from memory.)
+// this took 6.5: one token, 1024 x 4096, weights from memory.)
 // bfloat16: m16n8k16.  float32: m16n8k8 in tf32, three products, v = hi + lo with
 // hi the upper 11 bits: 22 bits an operand; the products of 32 k are added to sums
 // in float32, which round to nearest (the tensor core's cut off).
@@ -17,6 +17,9 @@
 // A block holds x in shared memory: two warps side by side along the features,
 // four along K; where x does not fit the blocks of a cluster split K further.
 // Sums are joined in a fixed order in float32; one rounding.
+//
+// From Python, one call after another: one token, 1024 x 4096, bfloat16 5.1 us (3.0 in a
+// graph, 5.6 TB/s), 20 rows, 800 x 2160, float32 6.7 us.
 //
 // Other rows (K no multiple of 8, float32: 4): fused multiply-adds, a warp
 // taking two features and up to eight tokens at a time, the lanes splitting K.

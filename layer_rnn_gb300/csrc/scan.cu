@@ -16,7 +16,10 @@
 // It needs h_{t-1}, which is not kept: the forward saves the state every
 // kScanState steps and the backward composes the rest of the tile again.
 //
-// Bound by memory: 10 to 20 flop for every 4 to 16 bytes.
+// Bound by memory: 10 to 20 flop for every 4 to 16 bytes.  512 x 128 x 1024 in
+// bfloat16 with output gate: forward 96 us (5.4 TB/s of the 512 MB that it needs), backward
+// 172 us (5.6 TB/s of 973 MB); the copy rate is 6.8.  One sequence of 65536 steps: 157
+// us, bound by the rounds of its clusters, 2.5 us each.
 #include <cuda.h>
 
 #include <algorithm>
@@ -868,7 +871,7 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
   if (stages && (!map(&p.gx, a.gx, a.D * G * a.H, a.ldg) || (a.dy && !map(&p.dy, a.dy, a.D * a.H, a.ldy))))
     return cudaErrorInvalidValue;
   // Blocks of a cluster share a channel group's tiles where the groups alone give
-  // the card less than two blocks an SM.  65536 x 1 x 1024 forward takes 158 us
+  // the card less than two blocks an SM.  65536 x 1 x 1024 forward takes 157 us
   // with clusters of 16; with eight warps a tile 232 us (two blocks an SM hold 14
   // such clusters, not 16).
   const int64_t groups = a.N * a.D * p.groups_h, tiles = (a.T + kTileSteps - 1) / kTileSteps;
@@ -887,7 +890,7 @@ cudaError_t run_tiles(K kernel, const ScanArgs& a, int planes, int stages, cudaS
 
 // Stages of the ring: two tiles in flight a block.  A third leaves room for
 // two blocks an SM instead of three and measured slower (65536 x 1 x 1024
-// forward 158 -> 222 us, 512 x 128 x 1024 training 353 -> 386 us).
+// forward 157 -> 222 us).
 template <typename E, bool GATE>
 cudaError_t forward_tiles(const ScanArgs& a, cudaStream_t st) {
   constexpr int planes = GATE ? 3 : 2, stages = GATE ? 2 : 3;
