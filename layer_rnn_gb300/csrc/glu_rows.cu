@@ -19,7 +19,7 @@
 // Sums are joined in a fixed order in float32; one rounding.
 //
 // From Python, one call after another: one token, 1024 x 4096, bfloat16 5.1 us (3.0 in a
-// graph, 5.6 TB/s), 20 rows, 800 x 2160, float32 6.7 us.
+// graph, its weights in L2), 20 rows, 800 x 2160, float32 6.7 us.
 //
 // Other rows (K no multiple of 8, float32: 4): fused multiply-adds, a warp
 // taking two features and up to eight tokens at a time, the lanes splitting K.

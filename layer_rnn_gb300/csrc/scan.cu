@@ -17,8 +17,8 @@
 // kScanState steps and the backward composes the rest of the tile again.
 //
 // Bound by memory: 10 to 20 flop for every 4 to 16 bytes.  512 x 128 x 1024 in
-// bfloat16 with output gate: forward 96 us (5.4 TB/s of the 512 MB that it needs), backward
-// 172 us (5.6 TB/s of 973 MB); the copy rate is 6.8.  One sequence of 65536 steps: 157
+// bfloat16 with output gate: forward 96 us (5.6 TB/s), backward 172
+// us (5.5 TB/s); the copy rate is 6.8.  One sequence of 65536 steps: 157
 // us, bound by the rounds of its clusters, 2.5 us each.
 #include <cuda.h>
 
